@@ -12,6 +12,10 @@ kernels.  PyTorch is used for device memory and streams only.
     conv_prefill(x, weight, bias, conv_state, out, cu_seqlens, max_len=..., ...)
     conv_qk_l2norm(x, qk_channels=..., head_dim=..., ...)
 
+What a layer runs behind the conv (linear attention with a decay for each head, the gated
+head norm, the norm at a block's end) is bound in linear_attention.py and reached from here
+too.
+
 Tensors (all on one GPU; bf16 or fp32 as the ABI allows):
     x, out       [n_seq, T, d_inner], or packed [total, d_inner] with cu_seqlens;
                  innermost stride 1, other strides free
@@ -34,12 +38,14 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from . import _lib
+from . import _lib, linear_attention
+from .linear_attention import *  # noqa: F401,F403
 
 __all__ = ["conv_verify_update", "conv_verify_update_dense", "conv_verify_update_dedup",
            "conv_verify_update_tree", "conv_verify_restore", "conv_prefill", "conv_qk_l2norm",
            "conv_verify_describe", "conv_verify_abi_version", "conv_verify_debug_count",
-           "write_count_library", "prepare", "CvError", "library_path", "LAYOUTS"]
+           "write_count_library", "prepare", "CvError", "library_path", "LAYOUTS",
+           *linear_attention.__all__]
 
 library_path = _lib.LIB_PATH
 LAYOUTS = {"dense": _lib.CV_WIN_DENSE, "dedup": _lib.CV_WIN_ROWS, "dedup_t": _lib.CV_WIN_ROWS_T}
@@ -357,10 +363,13 @@ def prepare(kind, *args, **kwargs):
 
     kind: "update" (the conv_verify_update arguments), "tree"
     (conv_verify_update_tree's), "restore", "prefill" or "l2"; or True / False for the
-    dedup / dense chain verify.  For tight launch loops (benchmarks, serving steps):
+    dedup / dense chain verify; or the name of an entry point of linear_attention.py, with
+    its arguments.  For tight launch loops (benchmarks, serving steps):
     each call is one ctypes call into the C ABI with the arguments built here, on the
     stream resolved here.  The tensors must stay alive while the callable is in use.
     """
+    if isinstance(kind, str) and kind in linear_attention.PREPARE:
+        return linear_attention.prepared(kind, args, kwargs)
     if kind is True or kind is False:
         x, weight, bias, conv_state, out, windows = args
         built = _verify_args("dedup" if kind else "dense", False, x, weight, bias, conv_state,

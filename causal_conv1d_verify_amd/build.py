@@ -1,4 +1,5 @@
-"""Builds libconvverify.so (HIP kernels for gfx950 + the C ABI) in-tree with hipcc.
+"""Builds libconvverify.so and liblinattn.so (HIP kernels for gfx950 + their C ABIs) in-tree
+with hipcc.
 
 Usage: python -m causal_conv1d_verify_amd.build   (or __graft_entry__.build())
 """
@@ -19,6 +20,8 @@ LIB = os.path.join(PKG, "libconvverify.so")
 # The write-count build (tests only): every global store also counts into registered
 # ranges (conv_verify_debug_count).  Its verify objects cover bf16 x and state only.
 LIB_WC = os.path.join(PKG, "libconvverify_wc.so")
+# Linear attention and the norms behind the conv: a library of its own, with its own C ABI.
+LIB_LA = os.path.join(PKG, "liblinattn.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -50,7 +53,11 @@ SOURCES_WC = [
     for tm in (0, 1) for v in (0, 1, 2, 3)
 ] + [("cv_aux_kernels.hip", "wc/cv_aux_kernels", [f"--offload-arch={ARCH}", *DEVICE_FLAGS, "-DCV_WRITE_COUNT"]),
      ("cv_api.cpp", "wc/cv_api", ["-DCV_WRITE_COUNT"])]
-MAX_JOBS = max(1, min(len(SOURCES) + len(SOURCES_WC), int(os.environ.get("MAX_JOBS", os.cpu_count() or 4))))
+SOURCES_LA = [
+    (f"la_{name}.hip", f"la_{name}", [f"--offload-arch={ARCH}", *DEVICE_FLAGS])
+    for name in ("recurrent", "norm")
+] + [("la_api.cpp", "la_api", [])]
+MAX_JOBS = max(1, min(len(SOURCES) + len(SOURCES_WC) + len(SOURCES_LA), int(os.environ.get("MAX_JOBS", os.cpu_count() or 4))))
 
 
 def _run(cmd):
@@ -62,12 +69,13 @@ def _run(cmd):
 
 
 def build(verbose: bool = True) -> str:
-    """Builds libconvverify.so and the write-count test library libconvverify_wc.so."""
+    """Builds libconvverify.so, the write-count test library libconvverify_wc.so and
+    liblinattn.so."""
     os.makedirs(os.path.join(BUILD, "wc"), exist_ok=True)
     t0 = time.time()
     pending = []
     libs = []
-    for sources, lib in ((SOURCES, LIB), (SOURCES_WC, LIB_WC)):
+    for sources, lib in ((SOURCES, LIB), (SOURCES_WC, LIB_WC), (SOURCES_LA, LIB_LA)):
         objs = []
         for src, stem, extra in sources:
             obj = os.path.join(BUILD, stem + ".o")
@@ -99,7 +107,7 @@ def build(verbose: bool = True) -> str:
         _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp])
         os.replace(tmp, lib)
     if verbose:
-        print(f"built {LIB} and {LIB_WC} in {time.time() - t0:.1f}s", file=sys.stderr)
+        print(f"built {LIB}, {LIB_WC} and {LIB_LA} in {time.time() - t0:.1f}s", file=sys.stderr)
     return LIB
 
 

@@ -1,0 +1,112 @@
+// Device-side helpers shared by the kernels of liblinattn.so.  Internal; included by the .hip
+// sources only.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cv_device.h"
+#include "la_internal.h"
+
+namespace laimpl {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+struct Bf16 { uint16_t bits; };
+
+// Two floats to packed bf16, to nearest even (one instruction on gfx950).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const bf16x2 p = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, p);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// N consecutive elements (N a multiple of 4 for float, 4 or a multiple of 8 for bf16) as floats.
+template <int N>
+__device__ __forceinline__ void load_vec(const float *p, float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(p + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i + j] = w[j];
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_vec(const Bf16 *p, float (&f)[N]) {
+    if constexpr (N == 4) {
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(p + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[i + 2 * j] = bf16_lo(w[j]), f[i + 2 * j + 1] = bf16_hi(w[j]);
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_vec(float *p, const float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const f32x4 w = {f[i], f[i + 1], f[i + 2], f[i + 3]};
+        *reinterpret_cast<f32x4 *>(p + i) = w;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_vec(Bf16 *p, const float (&f)[N]) {
+    if constexpr (N == 4) {
+        const u32x2 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+        *reinterpret_cast<u32x2 *>(p) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            const u32x4 w = {pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]),
+                             pack_bf16(f[i + 4], f[i + 5]), pack_bf16(f[i + 6], f[i + 7])};
+            *reinterpret_cast<u32x4 *>(p + i) = w;
+        }
+    }
+}
+
+// A log decay with -inf (and anything whose exp() is 0 many times over) made finite, so that
+// differences of sums of decays stay defined; NaN stays NaN.
+__device__ __forceinline__ float finite_decay(float g) { return g < -1e6f ? -1e6f : g; }
+
+// One row of a batch: its token count (-1: skip the row), its slot and its first elements.
+struct Row {
+    int n;
+    int64_t slot, q, k, v, o, g;
+};
+__device__ __forceinline__ Row row_of(const AttnArgs &a, int i) {
+    Row r;
+    r.slot = a.slot_idx ? a.slot_idx[i] : i;
+    int64_t first = 0, seq = i;
+    r.n = a.T;
+    if (a.cu_seqlens) {
+        first = a.cu_seqlens[i];
+        const int64_t n = (int64_t)a.cu_seqlens[i + 1] - first;
+        r.n = n >= 0 && n <= a.T ? (int)n : -1;
+        seq = 0;
+    } else if (a.num_tokens) {
+        const int n = a.num_tokens[i];
+        r.n = n >= 0 && n <= a.T ? n : -1;
+    }
+    if (r.slot < 0 || r.slot >= a.n_slots) r.n = -1;
+    r.q = seq * a.q_seq + first * a.q_tok;
+    r.k = seq * a.k_seq + first * a.k_tok;
+    r.v = seq * a.v_seq + first * a.v_tok;
+    r.o = seq * a.o_seq + first * a.o_tok;
+    r.g = seq * a.g_seq + first * a.g_tok;
+    return r;
+}
+
+}  // namespace
+}  // namespace laimpl

@@ -1,0 +1,58 @@
+// Shared by the host side (la_api.cpp) and the kernels of liblinattn.so: kernel arguments and
+// the pickers that map a launch plan to a compiled kernel.  Internal.
+#pragma once
+
+#include <stdint.h>
+
+namespace laimpl {
+
+constexpr int kWave = 64;
+
+// One batch of rows of the recurrence.  Strides in elements.
+struct AttnArgs {
+    const void *q, *k, *v;
+    const float *g;               // NULL: no decay
+    void *state;
+    void *out;                    // NULL: outputs not wanted
+    const int32_t *slot_idx;      // NULL: row i uses slot i
+    const int32_t *cu_seqlens;    // packed rows, or NULL
+    const int32_t *num_tokens;    // tokens of each row, or NULL (T)
+    const int32_t *has_init;      // NULL: every row starts from its state
+    int64_t q_seq, q_tok, q_head;
+    int64_t k_seq, k_tok, k_head;
+    int64_t v_seq, v_tok, v_head;
+    int64_t o_seq, o_tok, o_head;
+    int64_t g_seq, g_tok;
+    int64_t s_slot;
+    int32_t n_seq, T, v_heads, group;   // group = v heads that share a q/k head
+    int32_t dk, dv, n_slots, tiles;     // tiles = workgroups along dv of a head
+    float scale;
+    int32_t write_state;
+};
+
+struct NormArgs {
+    const void *y, *gate, *weight, *post_weight, *residual;
+    void *out, *residual_out;
+    int64_t rows;
+    int64_t y_row, y_head, gate_row, gate_head, out_row, out_head, res_row, res_out_row;
+    int32_t heads, dim;
+    float eps, scale;
+    int32_t sigmoid, gate_first;
+};
+
+// Columns of the state (channels of v) that one workgroup of the recurrent kernel holds.
+struct RecurrentPlan {
+    const void *fn;
+    int cols, threads;
+};
+// wide: 16 lanes across the state's columns (64 fp32 / 128 bf16 columns a workgroup), else 8.
+RecurrentPlan pick_recurrent(int x_bytes, int state_bytes, int dk, bool wide);
+
+struct NormPlan {
+    const void *fn;
+    int threads, per_block;       // groups (gated) or rows (residual) per workgroup
+};
+NormPlan pick_gated(int x_bytes, int dim);
+NormPlan pick_residual(int x_bytes, int res_bytes, int dim);
+
+}  // namespace laimpl
