@@ -41,7 +41,7 @@ class LaShape(ctypes.Structure):
         ("out_seq_stride", ctypes.c_int64), ("out_tok_stride", ctypes.c_int64),
         ("out_head_stride", ctypes.c_int64),
         ("g_seq_stride", ctypes.c_int64), ("g_tok_stride", ctypes.c_int64),
-        ("state_slot_stride", ctypes.c_int64),
+        ("state_slot_stride", ctypes.c_int64), ("tokens", ctypes.c_int64),
     ]
 
 

@@ -55,7 +55,7 @@ SOURCES_WC = [
      ("cv_api.cpp", "wc/cv_api", ["-DCV_WRITE_COUNT"])]
 SOURCES_LA = [
     (f"la_{name}.hip", f"la_{name}", [f"--offload-arch={ARCH}", *DEVICE_FLAGS])
-    for name in ("recurrent", "norm")
+    for name in ("chunked", "recurrent", "norm")
 ] + [("la_api.cpp", "la_api", [])]
 MAX_JOBS = max(1, min(len(SOURCES) + len(SOURCES_WC) + len(SOURCES_LA), int(os.environ.get("MAX_JOBS", os.cpu_count() or 4))))
 

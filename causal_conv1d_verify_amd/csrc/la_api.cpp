@@ -101,6 +101,7 @@ int check_attn(const la_shape_t *s, const Need &need, int *xb, int *sb, bool *em
     if (s->n_slots > 1 && s->state_slot_stride < per_slot)
         return fail(CV_EINVAL, "state_slot_stride (%lld) is below a slot's %lld elements",
                     (long long)s->state_slot_stride, (long long)per_slot);
+    if (need.packed && s->tokens < 0) return fail(CV_EINVAL, "tokens (%lld) is negative", (long long)s->tokens);
     if (need.out) {
         Dim d[3] = {{s->v_heads, s->out_head_stride}, {s->T, s->out_tok_stride},
                     {need.packed ? 1 : s->n_seq, s->out_seq_stride}};
@@ -166,6 +167,52 @@ int recurrent(laimpl::AttnArgs a, int xb, int sb, void *stream) {
     return launch(p.fn, heads * a.tiles, p.threads, 0, &a, stream);
 }
 
+// How packed prompts of bf16 tokens are cut.  A row's tokens are one chain of chunks in one
+// workgroup unless that chain is much longer than each of the chip's slots (two workgroups on
+// each of 256 compute units) would have of all chunks together: then rows are cut into segments
+// of about that share, at the price of passing over their k and v twice.
+struct Cut {
+    laimpl::ChunkedPlan plan;
+    int64_t tiles, segments, ws_states, ws_bytes;
+    int32_t seg_len;
+};
+Cut cut_prompts(const la_shape_t *s, int sb) {
+    constexpr int64_t kChunk = 64, kSlots = 512, kLeast = 4;
+    Cut c{};
+    c.plan = laimpl::pick_chunked(sb, s->dk, s->dv);
+    c.tiles = (s->dv + c.plan.cols - 1) / c.plan.cols;
+    c.segments = s->n_seq;
+    c.seg_len = s->T;
+    const int64_t heads = s->v_heads * c.tiles;
+    int64_t tokens = sat_mul(s->n_seq, s->T);
+    if (s->tokens > 0 && s->tokens < tokens) tokens = s->tokens;
+    const int64_t chain = (s->T + kChunk - 1) / kChunk;
+    const int64_t share = std::max(kLeast, sat_mul(tokens / kChunk + 1, heads) / kSlots);
+    if (chain <= share + share / 2 || chain <= 2 * kLeast) return c;
+    const int64_t segments = tokens / (share * kChunk) + s->n_seq;
+    const int64_t states = sat_mul(segments, heads);
+    if (states > INT32_MAX) return c;
+    c.seg_len = (int32_t)(share * kChunk);
+    c.segments = segments;
+    c.ws_states = states;
+    c.ws_bytes = sat_add(sat_mul(states, c.plan.ws_bytes), (4 * states + 15) / 16 * 16);
+    return c;
+}
+
+int chunked(laimpl::AttnArgs a, const Cut &c, void *workspace, void *stream) {
+    a.tiles = (int32_t)c.tiles;
+    a.seg_len = c.seg_len;
+    a.segments = (int32_t)c.segments;
+    a.ws = workspace;
+    a.ws_total = reinterpret_cast<float *>(static_cast<char *>(workspace) + c.ws_states * c.plan.ws_bytes);
+    const int64_t blocks = c.segments * a.v_heads * c.tiles;
+    if (c.ws_states) {
+        const int rc = launch(c.plan.first, blocks, 256, 0, &a, stream);
+        if (rc != CV_OK) return rc;
+    }
+    return launch(c.plan.run, blocks, 256, 0, &a, stream);
+}
+
 // update, verify and commit
 int few_tokens(const la_shape_t *s, const Need &need, const void *q, const void *k, const void *v, const float *g,
                const void *state, const int32_t *slot_idx, const int32_t *num_tokens, void *out, void *stream) {
@@ -225,7 +272,8 @@ int64_t linattn_prefill_workspace(const la_shape_t *s) {
     int xb, sb;
     bool empty;
     const int rc = check_attn(s, Need{true, true, true, false}, &xb, &sb, &empty);
-    return rc;
+    if (rc != CV_OK || empty || xb == 4) return rc;
+    return cut_prompts(s, sb).ws_bytes;
 }
 
 int linattn_prefill(const la_shape_t *s, const void *q, const void *k, const void *v, const float *g, void *state,
@@ -245,8 +293,9 @@ int linattn_prefill(const la_shape_t *s, const void *q, const void *k, const voi
                           {"slot_idx", slot_idx, false, 4}, {"has_initial_state", has_initial_state, false, 4}};
     if ((rc = check_pointers(ps)) != CV_OK) return rc;
     const int xb = dtype_bytes(s->x_dtype), sb = dtype_bytes(s->state_dtype);
-    return recurrent(attn_args(s, q, k, v, g, state, slot_idx, cu_seqlens, nullptr, has_initial_state, out, true),
-                     xb, sb, hip_stream);
+    const laimpl::AttnArgs a = attn_args(s, q, k, v, g, state, slot_idx, cu_seqlens, nullptr, has_initial_state, out, true);
+    if (xb == 4) return recurrent(a, xb, sb, hip_stream);
+    return chunked(a, cut_prompts(s, sb), workspace, hip_stream);
 }
 
 int linattn_update(const la_shape_t *s, const void *q, const void *k, const void *v, const float *g, void *state,

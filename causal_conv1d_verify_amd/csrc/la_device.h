@@ -108,5 +108,51 @@ __device__ __forceinline__ Row row_of(const AttnArgs &a, int i) {
     return r;
 }
 
+__device__ __forceinline__ float load_one(const float *p) { return *p; }
+__device__ __forceinline__ float load_one(const Bf16 *p) { return __uint_as_float((uint32_t)p->bits << 16); }
+__device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
+__device__ __forceinline__ void store_one(Bf16 *p, float x) {
+    p->bits = __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+// Segment `id` of the rows in order, each row cut into ceil(tokens / seg_len) of them and one
+// where it has no tokens; row -1 where there are fewer.  Rows that are skipped have none, nor
+// has a row that would end past a.segments (more tokens than the caller declared).  Called by
+// a whole workgroup of 256, `shared` is two words of LDS.
+struct Segment { int row, index; bool last; };
+__device__ __forceinline__ int segments_of(const AttnArgs &a, int i) {
+    const Row r = row_of(a, i);
+    return r.n < 0 ? 0 : r.n == 0 ? 1 : (int)(((int64_t)r.n + a.seg_len - 1) / a.seg_len);
+}
+__device__ __forceinline__ Segment find_segment(const AttnArgs &a, int id, int64_t *shared) {
+    if (a.seg_len >= a.T) return row_of(a, id).n < 0 ? Segment{-1, 0, true} : Segment{id, 0, true};
+    __shared__ int sums[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t before = 0;                            // segments of the rows before these 256
+    if (threadIdx.x == 0) shared[0] = -1;
+    for (int i0 = 0; i0 < a.n_seq && before <= id; i0 += 256) {
+        const int i = i0 + threadIdx.x;
+        const int own = i < a.n_seq ? segments_of(a, i) : 0;
+        int upto = own;
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int y = __shfl_up(upto, d);
+            if (lane >= d) upto += y;
+        }
+        __syncthreads();                           // the sums of the last turn are read
+        if (lane == kWave - 1) sums[wave] = upto;
+        __syncthreads();
+        int64_t at = before + upto - own;
+        for (int w = 0; w < wave; ++w) at += sums[w];
+        if (id >= at && id < at + own && at + own <= a.segments) {
+            shared[0] = i;
+            shared[1] = (id - at) * 2 + (id - at == own - 1);
+        }
+        for (int w = 0; w < 4; ++w) before += sums[w];
+    }
+    __syncthreads();
+    return Segment{(int)shared[0], (int)(shared[1] >> 1), (shared[1] & 1) != 0};
+}
+
 }  // namespace
 }  // namespace laimpl

@@ -28,6 +28,11 @@ struct AttnArgs {
     int32_t dk, dv, n_slots, tiles;     // tiles = workgroups along dv of a head
     float scale;
     int32_t write_state;
+    // prompts in chunks: a row is cut into segments of seg_len tokens (a multiple of the chunk;
+    // rows of at most seg_len tokens are one)
+    int32_t seg_len, segments;          // segments that the grid and the workspace hold
+    void *ws;                           // what each segment but a row's last adds to a state
+    float *ws_total;                    // and the decay over it
 };
 
 struct NormArgs {
@@ -47,6 +52,15 @@ struct RecurrentPlan {
 };
 // wide: 16 lanes across the state's columns (64 fp32 / 128 bf16 columns a workgroup), else 8.
 RecurrentPlan pick_recurrent(int x_bytes, int state_bytes, int dk, bool wide);
+
+// Prompts in chunks.  `first` leaves what a segment adds to a state in the workspace, `run`
+// makes the outputs and the last state.
+struct ChunkedPlan {
+    const void *run, *first;
+    int cols;                     // columns of the state per workgroup of 256 lanes
+    int64_t ws_bytes;             // of one workgroup's state
+};
+ChunkedPlan pick_chunked(int state_bytes, int dk, int dv);
 
 struct NormPlan {
     const void *fn;

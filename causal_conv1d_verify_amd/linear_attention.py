@@ -154,7 +154,8 @@ def _attn_args(kind, q, k, v, g, state, out, *, cu_seqlens=None, max_len=None, s
     shape = _linattn.LaShape(
         n_seq, T, q_heads, v_heads, dk, dv, dk ** -0.5 if scale is None else scale,
         _dtype_code(v), _dtype_code(state), state.shape[0], *strides(q), *strides(k),
-        *strides(v), *strides(out), g_seq, g_tok, _strides(state, (0,))[0])
+        *strides(v), *strides(out), g_seq, g_tok, _strides(state, (0,))[0],
+        v.shape[0] if packed else 0)
     handle = _on_stream(stream, dev)
     ref = ctypes.byref(shape)
     if packed and n_seq and v.shape[0] == 0:

@@ -75,13 +75,16 @@ typedef struct la_shape {
     int64_t out_seq_stride, out_tok_stride, out_head_stride;
     int64_t g_seq_stride, g_tok_stride;
     int64_t state_slot_stride;   /* >= v_heads*dk*dv if n_slots > 1                         */
+    int64_t tokens;       /* prefill: tokens of all rows together, or 0 if that is not known;
+                             sizes the grid and the workspace                               */
 } la_shape_t;
 
 /*
  * Packed prompts.  Row i holds cu_seqlens[i+1] - cu_seqlens[i] tokens (0..T; other counts:
  * the row is skipped).  It starts from its slot's state, or from zeros where
  * has_initial_state[i] == 0 (NULL: all 1), and its slot is left with the state after its last
- * token (a row of no tokens: with its starting state).
+ * token (a row of no tokens: with its starting state).  Where shape->tokens is given, rows in
+ * order that would hold more than that together may be skipped.
  * workspace: linattn_prefill_workspace(shape) bytes (16-byte aligned; NULL if that is 0), free
  * again once the call's work on the stream is done.
  */
