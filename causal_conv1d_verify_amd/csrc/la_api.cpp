@@ -123,9 +123,9 @@ int check_pointers(const Pointer (&ps)[N]) {
     return CV_OK;
 }
 
-int launch(const void *fn, int64_t blocks, int threads, int64_t lds, void *args, void *stream) {
+int launch(const void *fn, int64_t blocks, int threads, int64_t lds, void *args, void *stream, void *more = nullptr) {
     if (blocks > INT32_MAX) return fail(CV_ENOTSUP, "%lld workgroups in one launch", (long long)blocks);
-    void *kargs[] = {args};
+    void *kargs[] = {args, more};
     const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3((unsigned)threads), kargs,
                                          (size_t)lds, (hipStream_t)stream);
     if (e != hipSuccess)
@@ -167,19 +167,26 @@ int recurrent(laimpl::AttnArgs a, int xb, int sb, void *stream) {
     return launch(p.fn, heads * a.tiles, p.threads, 0, &a, stream);
 }
 
-// How packed prompts of bf16 tokens are cut.  A row's tokens are one chain of chunks in one
-// workgroup unless that chain is much longer than each of the chip's slots (two workgroups on
-// each of 256 compute units) would have of all chunks together: then rows are cut into segments
-// of about that share, at the price of passing over their k and v twice.
+// How packed prompts of bf16 tokens are cut into workgroups.
+//
+// Along a row: its tokens are one chain of chunks in one workgroup unless that chain is much
+// longer than the share of all chunks that each of the chip's slots would have (two workgroups on
+// each of 256 compute units): then rows are cut into segments of about that share, at the price
+// of passing over their k and v twice (one prompt of 16384 with 32 heads: 202 us in 16
+// segments).
+//
+// Across a head: tiles of 128 columns, since what a chunk reads and the products q.k serve all of
+// a tile; tiles of 64 where the wide ones would leave most compute units empty (64 workgroups of
+// 32 chunks: 122 us for 160).
 struct Cut {
     laimpl::ChunkedPlan plan;
     int64_t tiles, segments, ws_states, ws_bytes;
     int32_t seg_len;
 };
-Cut cut_prompts(const la_shape_t *s, int sb) {
+Cut cut_prompts(const la_shape_t *s, int sb, bool wide) {
     constexpr int64_t kChunk = 64, kSlots = 512, kLeast = 4;
     Cut c{};
-    c.plan = laimpl::pick_chunked(sb, s->dk, s->dv);
+    c.plan = laimpl::pick_chunked(sb, s->dk, wide);
     c.tiles = (s->dv + c.plan.cols - 1) / c.plan.cols;
     c.segments = s->n_seq;
     c.seg_len = s->T;
@@ -188,15 +195,24 @@ Cut cut_prompts(const la_shape_t *s, int sb) {
     if (s->tokens > 0 && s->tokens < tokens) tokens = s->tokens;
     const int64_t chain = (s->T + kChunk - 1) / kChunk;
     const int64_t share = std::max(kLeast, sat_mul(tokens / kChunk + 1, heads) / kSlots);
-    if (chain <= share + share / 2 || chain <= 2 * kLeast) return c;
     const int64_t segments = tokens / (share * kChunk) + s->n_seq;
     const int64_t states = sat_mul(segments, heads);
-    if (states > INT32_MAX) return c;
-    c.seg_len = (int32_t)(share * kChunk);
-    c.segments = segments;
-    c.ws_states = states;
-    c.ws_bytes = sat_add(sat_mul(states, c.plan.ws_bytes), (4 * states + 15) / 16 * 16);
+    if (chain > share + share / 2 && chain > 2 * kLeast && states <= INT32_MAX) {
+        c.seg_len = (int32_t)(share * kChunk);
+        c.segments = segments;
+        c.ws_states = states;
+        c.ws_bytes = sat_add(sat_mul(states, c.plan.ws_bytes), (4 * states + 15) / 16 * 16);
+    }
+    if (wide && c.segments * heads <= 128) return cut_prompts(s, sb, false);
     return c;
+}
+Cut cut_prompts(const la_shape_t *s, int sb) { return cut_prompts(s, sb, s->dv > 64); }
+
+// Whether prompts go in chunks: bf16 tokens whose chunk lies within 32-bit offsets.  (Tokens
+// 32 MiB and more apart go one by one.)
+bool in_chunks(const la_shape_t *s, int xb) {
+    const int64_t far = std::max(std::max(s->q_tok_stride, s->k_tok_stride), std::max(s->v_tok_stride, s->out_tok_stride));
+    return xb == 2 && far < (1 << 24);
 }
 
 int chunked(laimpl::AttnArgs a, const Cut &c, void *workspace, void *stream) {
@@ -207,10 +223,14 @@ int chunked(laimpl::AttnArgs a, const Cut &c, void *workspace, void *stream) {
     a.ws_total = reinterpret_cast<float *>(static_cast<char *>(workspace) + c.ws_states * c.plan.ws_bytes);
     const int64_t blocks = c.segments * a.v_heads * c.tiles;
     if (c.ws_states) {
-        const int rc = launch(c.plan.first, blocks, 256, 0, &a, stream);
+        int rc = launch(c.plan.first, blocks, c.plan.threads, 0, &a, stream);
+        if (rc != CV_OK) return rc;
+        int vectors = (int)(c.plan.ws_bytes / 16);
+        rc = launch(c.plan.combine, (int64_t)a.n_seq * a.v_heads * c.tiles * (vectors / c.plan.threads), c.plan.threads,
+                    0, &a, stream, &vectors);
         if (rc != CV_OK) return rc;
     }
-    return launch(c.plan.run, blocks, 256, 0, &a, stream);
+    return launch(c.plan.run, blocks, c.plan.threads, 0, &a, stream);
 }
 
 // update, verify and commit
@@ -272,7 +292,7 @@ int64_t linattn_prefill_workspace(const la_shape_t *s) {
     int xb, sb;
     bool empty;
     const int rc = check_attn(s, Need{true, true, true, false}, &xb, &sb, &empty);
-    if (rc != CV_OK || empty || xb == 4) return rc;
+    if (rc != CV_OK || empty || !in_chunks(s, xb)) return rc;
     return cut_prompts(s, sb).ws_bytes;
 }
 
@@ -294,7 +314,7 @@ int linattn_prefill(const la_shape_t *s, const void *q, const void *k, const voi
     if ((rc = check_pointers(ps)) != CV_OK) return rc;
     const int xb = dtype_bytes(s->x_dtype), sb = dtype_bytes(s->state_dtype);
     const laimpl::AttnArgs a = attn_args(s, q, k, v, g, state, slot_idx, cu_seqlens, nullptr, has_initial_state, out, true);
-    if (xb == 4) return recurrent(a, xb, sb, hip_stream);
+    if (!in_chunks(s, xb)) return recurrent(a, xb, sb, hip_stream);
     return chunked(a, cut_prompts(s, sb), workspace, hip_stream);
 }
 

@@ -43,27 +43,14 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// x less the low (high) bf16 of w, exact: one dot product with (-1, 0) or (0, -1), which are kept
-// in scalar registers (as an inline constant of a packed operand they would mean something else).
-__device__ __forceinline__ float less_lo(float x, uint32_t w) {
-    uint32_t m = 0xBF80u;
-    asm("" : "+s"(m));
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, m), x, false);
-}
-__device__ __forceinline__ float less_hi(float x, uint32_t w) {
-    uint32_t m = 0xBF800000u;
-    asm("" : "+s"(m));
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, m), x, false);
-}
-
 // The next bf16 part of eight values, taken off them.
 __device__ __forceinline__ bf16x8 take_part(float (&x)[8]) {
     u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        x[2 * i] = less_lo(x[2 * i], w[i]);
-        x[2 * i + 1] = less_hi(x[2 * i + 1], w[i]);
+        x[2 * i] -= bf16_lo(w[i]);
+        x[2 * i + 1] -= bf16_hi(w[i]);
     }
     return __builtin_bit_cast(bf16x8, w);
 }
@@ -82,27 +69,62 @@ __device__ __forceinline__ bf16x8 take_bad(bf16x8 &v) {
     return __builtin_bit_cast(bf16x8, bad);
 }
 
+// The vector work of a step between its M matrix instructions, V to each.
+template <int M, int V>
+__device__ __forceinline__ void in_turn() {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // a matrix instruction
+        __builtin_amdgcn_sched_group_barrier(0x002, V, 0);     // vector instructions
+    }
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_from(double x) {
+    const uint64_t w = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)w, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(w >> 32), CTRL, ROWS, 0xF, false);
+    return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// The sum over the lanes up to each one, by data moves between lanes: inside rows of 16 from 1, 2,
+// 4 and 8 lanes before (zeros from outside), then row 0's to row 1 and 2's to 3, then 0 and 1's
+// to 2 and 3.
+__device__ __forceinline__ double running_sum(double x) {
+    x = add_from<0x111, 0xF>(x);
+    x = add_from<0x112, 0xF>(x);
+    x = add_from<0x114, 0xF>(x);
+    x = add_from<0x118, 0xF>(x);
+    x = add_from<0x142, 0xA>(x);
+    return add_from<0x143, 0xC>(x);
+}
+
 struct __attribute__((aligned(16))) Decays {   // of one chunk
     float hi[C], lo[C];            // running sums in base 2, as pairs
     float in[C], left[C];          // scale * 2^(sum up to t), 2^(sum behind t)
     float total;                   // 2^(sum of all)
 };
 
+constexpr int W = 4;               // wavefronts of a workgroup
+
 template <int KT, int NC>
 struct Shared {
-    static constexpr int QP = KT * 64 + 16, KP = KT * 64 + 32, VP = NC * 128 + 32, PP = C * 2 + 16;
-    __attribute__((aligned(16))) char q[C * QP], k[C * KP], v[C * VP], p[2][C * PP];
+    static constexpr int QP = KT * 64 + 16, KP = KT * 64 + 32, VP = W * NC * 32 + 32, PP = C * 2 + 16;
+    // the decayed products, in two parts, take q's place once q has been used
+    union __attribute__((aligned(16))) { char q[C * QP]; char p[2][C * PP]; };
+    __attribute__((aligned(16))) char k[C * KP], v[C * VP], zeros[16];
     Decays d[2];
     int64_t found[2];
 };
 
-// KT: dk in blocks of 32; NC: column tiles of 16 per wavefront; OUT: outputs are wanted, else
+// KT: dk in blocks of 32; W: wavefronts; NC: column tiles of 16 of each; OUT: outputs are wanted, else
 // only what a segment's tokens leave in a state that starts from zeros.
 template <int KT, int NC, typename ST, bool OUT>
-__global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a) {
+__global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(const AttnArgs a) {
     constexpr int PARTS = sizeof(ST) == 4 ? 3 : 2;
     constexpr int DT = 2 * KT;                     // row tiles of the state
     using SH = Shared<KT, NC>;
+    constexpr int COLS = 16 * W * NC;
     __shared__ SH sh;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -113,20 +135,20 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
     const int h = rest % a.v_heads, id = rest / a.v_heads;
     const int hq = h / a.group;
 
-    const Segment seg = find_segment(a, id, sh.found);
+    const Segment seg = find_segment<W>(a, id, sh.found);
     if (seg.row < 0) return;                       // same for the workgroup
-    const Row row = row_of(a, seg.row);
-    const bool init = !a.has_init || a.has_init[seg.row] != 0;
+    const Row row = uniform(row_of(a, seg.row));
+    const bool init = !a.has_init || uniform(a.has_init[seg.row]) != 0;
     if (!OUT && seg.last) return;
     if (OUT && row.n == 0 && init) return;
     const int first = seg.index * a.seg_len;
     const int n = (row.n - first < a.seg_len ? row.n - first : a.seg_len);
 
-    const int col0 = tile * 64 * NC;               // of the workgroup
+    const int col0 = tile * COLS;                 // of the workgroup
     const int colw = 16 * NC * wave;               // of the wavefront, inside the tile
-    auto column = [&](int nc) {                    // of lane j's column of tile nc, inside the tile
-        return NC == 2 ? colw + 8 * (j / 4) + 4 * nc + j % 4 : colw + j;
-    };
+    // of column x of the wavefront's tile nc: with two tiles, groups of 4 in turn, so that the
+    // outputs of a lane are 4 * NC columns side by side
+    auto column = [&](int nc, int x) { return NC == 2 ? colw + 8 * (x / 4) + 4 * nc + x % 4 : colw + x; };
 
     // ---- the state that enters the segment
     f32x4 S[NC][DT];
@@ -137,7 +159,7 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
         for (int d = 0; d < DT; ++d) {
             S[nc][d] = f32x4{0, 0, 0, 0};
             if (!OUT || !init) continue;
-            const int c = col0 + column(nc);
+            const int c = col0 + column(nc, j);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 16 * d + g4 + i;
@@ -146,17 +168,17 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
         }
     const int64_t ws_head = ((int64_t)id * a.v_heads + h) * a.tiles + tile;
     const int64_t ws_step = (int64_t)a.v_heads * a.tiles;          // from segment to segment
-    constexpr int64_t WS = (int64_t)256 * NC * DT;                 // f32x4 of one workgroup
+    constexpr int64_t WS = (int64_t)64 * W * NC * DT;              // f32x4 of one workgroup
     if constexpr (OUT) {
-        for (int s = seg.index; s > 0; --s) {
-            const int64_t at = ws_head - s * ws_step;
-            const float keep = a.ws_total[at];
-            const f32x4 *w = static_cast<const f32x4 *>(a.ws) + at * WS + tid;
+        if (seg.index > 0) {                       // what the segments before leave, and their decay
+            float keep = 1.0f;
+            for (int s = seg.index; s > 0; --s) keep *= a.ws_total[ws_head - s * ws_step];
+            const f32x4 *w = static_cast<const f32x4 *>(a.ws) + (ws_head - ws_step) * WS + tid;
 #pragma unroll
             for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
-                    const f32x4 x = w[(nc * DT + d) * 256];
+                    const f32x4 x = w[(nc * DT + d) * 64 * W];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) S[nc][d][i] = fmaf(S[nc][d][i], keep, x[i]);
                 }
@@ -164,83 +186,51 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
     }
 
     // ---- staging of a chunk: global memory -> registers -> LDS.  Eight lanes take 128 bytes of a
-    // row, so a thread has two rows (r0 = thread / 8 and r0 + 32) and the same channels of each block.  Rows
-    // and channels that are not there are read from the last ones that are, and zeroed on the
-    // way to LDS.
-    u32x4 rq[OUT ? KT : 1], rk[KT], rv[2 * NC];
-    const Bf16 *gq = static_cast<const Bf16 *>(a.q) + row.q + hq * a.q_head + first * a.q_tok;
-    const Bf16 *gk = static_cast<const Bf16 *>(a.k) + row.k + hq * a.k_head + first * a.k_tok;
-    const Bf16 *gv = static_cast<const Bf16 *>(a.v) + row.v + h * a.v_head + col0 + first * a.v_tok;
-    const int dv_here = a.dv - col0 < 64 * NC ? a.dv - col0 : 64 * NC;
-    const bool whole_tile = a.dk == 32 * KT && dv_here == 64 * NC;
-    auto fetch = [&](int left, int place) {        // the chunk at gq, gk, gv: `left` tokens of it on
-        const int r0 = place >> 3, c0 = 8 * (place & 7);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = r0 + 32 * u < left ? r0 + 32 * u : left - 1;
-            const Bf16 *pk = gk + r * a.k_tok, *pv = gv + r * a.v_tok, *pq = OUT ? gq + r * a.q_tok : nullptr;
-#pragma unroll
-            for (int b = 0; b < KT / 2; ++b) {
-                const int c = c0 + 64 * b < a.dk ? c0 + 64 * b : 0;
-                rk[u * (KT / 2) + b] = *reinterpret_cast<const u32x4 *>(pk + c);
-                if constexpr (OUT) rq[u * (KT / 2) + b] = *reinterpret_cast<const u32x4 *>(pq + c);
-            }
-#pragma unroll
-            for (int b = 0; b < NC; ++b) {
-                const int c = c0 + 64 * b < dv_here ? c0 + 64 * b : 0;
-                rv[u * NC + b] = *reinterpret_cast<const u32x4 *>(pv + c);
-            }
-        }
-        gk += C * a.k_tok;
-        gv += C * a.v_tok;
-        if constexpr (OUT) gq += C * a.q_tok;
+    // row, so a thread has 8 / W rows (from thread / 8 on, 8 * W apart) and the same channels of
+    // each block of 64.  Rows and channels that are not there are read from the last ones that
+    // are, and zeroed on the way to LDS.
+    constexpr int U = 8 / W, B = KT / 2, VB = W * NC / 4;   // rows; blocks of q and k, of v
+    u32x4 rq[U][OUT ? B : 1], rk[U][B], rv[U][VB];
+    const char *gq = reinterpret_cast<const char *>(static_cast<const Bf16 *>(a.q) + row.q + hq * a.q_head + first * a.q_tok);
+    const char *gk = reinterpret_cast<const char *>(static_cast<const Bf16 *>(a.k) + row.k + hq * a.k_head + first * a.k_tok);
+    const char *gv = reinterpret_cast<const char *>(static_cast<const Bf16 *>(a.v) + row.v + h * a.v_head + col0 + first * a.v_tok);
+    // bytes from token to token; a chunk's fit 32 bits
+    const uint32_t q_step = 2 * (uint32_t)a.q_tok, k_step = 2 * (uint32_t)a.k_tok, v_step = 2 * (uint32_t)a.v_tok;
+    const int dv_here = a.dv - col0 < COLS ? a.dv - col0 : COLS;
+    const bool whole_tile = a.dk == 32 * KT && dv_here == COLS;
+    // Piece `i` (row i / BLOCKS, block i % BLOCKS) of a chunk of which `left` tokens are there.
+    auto fetch = [&](const char *from, uint32_t step, int here, auto &to, int i, int left, int place) {
+        constexpr int BLOCKS = sizeof(to[0]) / sizeof(u32x4);
+        const int u = i / BLOCKS, b = i % BLOCKS, row = (place >> 3) + 8 * W * u, c = 8 * (place & 7) + 64 * b;
+        const uint32_t t = row < left ? row : left - 1;
+        to[u][b] = *reinterpret_cast<const u32x4 *>(from + (t * step + (c < here ? 2 * c : 0)));
     };
-    auto stage = [&](int left, int place) {
+    auto stage = [&](char *lds, int pitch, int here, auto &from, int left, int place) {
+        constexpr int BLOCKS = sizeof(from[0]) / sizeof(u32x4);
         const int r0 = place >> 3, c0 = 8 * (place & 7);
         if (!whole_tile || left < C) {
-            const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const bool there = r0 + 32 * u < left;
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int b = 0; b < KT / 2; ++b)
-                    if (!there || c0 + 64 * b >= a.dk) {
-                        rk[u * (KT / 2) + b] = zero;
-                        if constexpr (OUT) rq[u * (KT / 2) + b] = zero;
-                    }
-#pragma unroll
-                for (int b = 0; b < NC; ++b)
-                    if (!there || c0 + 64 * b >= dv_here) rv[u * NC + b] = zero;
-            }
+                for (int b = 0; b < BLOCKS; ++b)
+                    if (r0 + 8 * W * u >= left || c0 + 64 * b >= here) from[u][b] = u32x4{0, 0, 0, 0};
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = r0 + 32 * u;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int b = 0; b < KT / 2; ++b) {
-                *reinterpret_cast<u32x4 *>(sh.k + r * SH::KP + 2 * c0 + 128 * b) = rk[u * (KT / 2) + b];
-                if constexpr (OUT)
-                    *reinterpret_cast<u32x4 *>(sh.q + r * SH::QP + 2 * c0 + 128 * b) = rq[u * (KT / 2) + b];
-            }
-#pragma unroll
-            for (int b = 0; b < NC; ++b)
-                *reinterpret_cast<u32x4 *>(sh.v + r * SH::VP + 2 * c0 + 128 * b) = rv[u * NC + b];
-        }
+            for (int b = 0; b < BLOCKS; ++b)
+                *reinterpret_cast<u32x4 *>(lds + (r0 + 8 * W * u) * pitch + 2 * c0 + 128 * b) = from[u][b];
     };
     // One wavefront, lane = token: the chunk's decays, from log decays loaded a chunk earlier.
-    const float *gg = a.g ? a.g + row.g + h + (int64_t)(first + lane) * a.g_tok : nullptr;
+    const float *gg = a.g ? a.g + row.g + h + (int64_t)first * a.g_tok : nullptr;
     float g_next = 0.0f;
     auto fetch_decays = [&](int t0) {
-        g_next = gg && t0 + lane < n ? gg[(int64_t)t0 * a.g_tok] : 0.0f;
+        if (gg) g_next = t0 + lane < n ? gg[(int64_t)(t0 + lane) * a.g_tok] : 0.0f;
     };
     double whole = 0.0;                            // log2 of the segment's decay (that wavefront)
     auto scan = [&](Decays &d) {
         double x = 1.4426950408889634 * (double)finite_decay(g_next);
-#pragma unroll
-        for (int s = 1; s < C; s *= 2) {
-            const double y = __shfl_up(x, s);
-            if (lane >= s) x += y;
-        }
+        x = running_sum(x);
         const double total = __shfl(x, C - 1);
         const float hi = (float)x;
         d.hi[lane] = hi;
@@ -252,85 +242,93 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
     };
 
     if (n > 0) {
-        if (wave == 3) fetch_decays(0);
-        fetch(n, tid);
-        if (wave == 3) {
-            scan(sh.d[0]);
-            fetch_decays(C);
-        }
+        fetch_decays(0);
+#pragma unroll
+        for (int i = 0; i < KT; ++i) fetch(gk, k_step, a.dk, rk, i, n, tid);
+#pragma unroll
+        for (int i = 0; i < U * VB; ++i) fetch(gv, v_step, dv_here, rv, i, n, tid);
+        if constexpr (OUT)
+#pragma unroll
+            for (int i = 0; i < KT; ++i) fetch(gq, q_step, a.dk, rq, i, n, tid);
+        if (wave == W - 1) scan(sh.d[0]);
+        stage(sh.k, SH::KP, a.dk, rk, n, tid);
+        stage(sh.v, SH::VP, dv_here, rv, n, tid);
     }
-    if constexpr (OUT) {
-        // the tiles just above the diagonal that the products read: zeros for good
-        const int t = 32 * (tid >> 7) + ((tid >> 3) & 15), c = 16 + (tid & 7) * 2;
-        const int at = t * SH::PP + (32 * (tid >> 7) + c) * 2;
-        *reinterpret_cast<uint32_t *>(sh.p[0] + at) = 0;
-        *reinterpret_cast<uint32_t *>(sh.p[1] + at) = 0;
-    }
-    Bf16 *out = OUT ? static_cast<Bf16 *>(a.out) + row.o + h * a.o_head + col0 : nullptr;
+    if (tid < 4) reinterpret_cast<uint32_t *>(sh.zeros)[tid] = 0;
+    char *out = OUT ? reinterpret_cast<char *>(static_cast<Bf16 *>(a.out) + row.o + h * a.o_head + col0 + first * a.o_tok)
+                    : nullptr;
+    const uint32_t o_step = 2 * (uint32_t)a.o_tok;
 
+    // Each step below issues matrix instructions whose operands the step before it made, and
+    // between them the vector work and the reads that the next step needs: a wavefront issues in
+    // order, and there are few of them.
     for (int t0 = 0, turn = 0; t0 < n; t0 += C, turn ^= 1) {
         // The lane's place, hidden at each chunk: what is derived from it is computed again
         // rather than kept in registers, which are short here.
         int place = tid;
         asm volatile("" : "+v"(place));
         const int j = place & 15, g4 = (place & 48) >> 2;
-        stage(n - t0, place);
-        __syncthreads();
-        const Decays &dec = sh.d[turn];
-        if (wave == 3 && t0 + C < n) {
-            scan(sh.d[turn ^ 1]);
-            fetch_decays(t0 + 2 * C);
+        // the next chunk (this one again behind the last: what is fetched then is not used)
+        const bool more = n - t0 > C;
+        const int next = more ? n - t0 - C : n - t0;
+        if (more) {
+            gk += (int64_t)C * k_step;
+            gv += (int64_t)C * v_step;
+            if constexpr (OUT) gq += (int64_t)C * q_step;
         }
+        if constexpr (OUT) stage(sh.q, SH::QP, a.dk, rq, n - t0, place);
+        __syncthreads();                           // the chunk is there
+        fetch_decays(t0 + C);
+        const Decays &dec = sh.d[turn];
+        const float keep = dec.total;
 
-        f32x4 o[OUT ? 4 : 1][NC];
+        auto read_v = [&](int nc, int x, int j) {  // this lane's tokens of the wavefront's columns
+            const char *vp = sh.v + (32 * x + 2 * g4 + j / 4) * SH::VP + 2 * column(nc, 4 * (j % 4));
+            return frag(read_transposed(vp), read_transposed(vp + 4 * SH::VP));
+        };
+        bf16x8 part[2][NC][PARTS];                 // decayed values, of 32 tokens at a time
+        bf16x8 raw;
+        float left[8];
+        auto read_for_decay = [&](int x, int nc) {
+            raw = read_v(nc, x, j);
+            load_vec<8>(dec.left + 32 * x + 2 * g4, left);
+        };
+        auto decay_v = [&](int x, int nc) {
+            const u32x4 w = __builtin_bit_cast(u32x4, raw);
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = bf16_lo(w[i]) * left[2 * i];
+                f[2 * i + 1] = bf16_hi(w[i]) * left[2 * i + 1];
+            }
+#pragma unroll
+            for (int u = 0; u < PARTS; ++u) part[x][nc][u] = take_part(f);
+        };
+
+        f32x4 o[OUT ? 4 : 1][NC];                  // outputs, transposed: lane = token, 4 columns
+        f32x4 p[OUT ? 3 : 1];                      // products q.k, transposed: lane = token t
+        int ti[3], si[3];
         if constexpr (OUT) {
-            // ---- this wavefront's tiles of the decayed products, transposed (lane = token t):
-            // 3 or (the one that scans) 1 of the ten, (3, 0..2); (2, 0..2); (1, 0..1), (3, 3); (0, 0)
-            auto products = [&](auto tiles) {
-                constexpr int N = decltype(tiles)::value;
-                f32x4 p[N];
-                int ti[N], si[N];
+            // ---- q.k: of the ten tiles on and below the diagonal, three wavefronts make three each,
+            // (3, 0..2); (2, 0..2); (1, 0..1), (3, 3), and the one that sums the next chunk's
+            // decays has (0, 0) (three times, so that all run the same code)
 #pragma unroll
-                for (int u = 0; u < N; ++u) {
-                    const bool lone = wave == 2 && u == 2;
-                    ti[u] = lone ? 3 : 3 - wave;
-                    si[u] = lone ? 3 : u;
-                    p[u] = f32x4{0, 0, 0, 0};
-                }
+            for (int u = 0; u < 3; ++u) {
+                const bool third = wave == 2 && u == 2;
+                ti[u] = third ? 3 : 3 - wave;
+                si[u] = third ? 3 : wave == 3 ? 0 : u;
+                p[u] = f32x4{0, 0, 0, 0};
+            }
 #pragma unroll
-                for (int x = 0; x < KT; ++x)
+            for (int x = 0; x < KT; ++x)
 #pragma unroll
-                    for (int u = 0; u < N; ++u)
-                        p[u] = mma(*reinterpret_cast<const bf16x8 *>(sh.k + (16 * si[u] + j) * SH::KP + 4 * g4 + 64 * x),
-                                   *reinterpret_cast<const bf16x8 *>(sh.q + (16 * ti[u] + j) * SH::QP + 4 * g4 + 64 * x),
-                                   p[u]);
-#pragma unroll
-                for (int u = 0; u < N; ++u) {
-                    const int t = 16 * ti[u] + j, s = 16 * si[u] + g4;
-                    const float thi = dec.hi[t], tlo = dec.lo[t];
-                    const f32x4 shi = *reinterpret_cast<const f32x4 *>(dec.hi + s);
-                    const f32x4 slo = *reinterpret_cast<const f32x4 *>(dec.lo + s);
-                    float f[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float e = __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i]));
-                        f[i] = s + i <= t ? a.scale * p[u][i] * e : 0.0f;
-                    }
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        const u32x2 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
-                        *reinterpret_cast<u32x2 *>(sh.p[part] + t * SH::PP + 2 * s) = w;
-                        f[0] = less_lo(f[0], w[0]), f[1] = less_hi(f[1], w[0]);
-                        f[2] = less_lo(f[2], w[1]), f[3] = less_hi(f[3], w[1]);
-                    }
-                }
-            };
-            if (wave == 3) products(std::integral_constant<int, 1>{});
-            else products(std::integral_constant<int, 3>{});
-
-            // ---- S^T q, transposed outputs: lane = token, registers = 4 columns.  q is read one
-            // step ahead; a product's accumulator comes round after 4 * NC products.
+                for (int u = 0; u < 3; ++u)
+                    p[u] = mma(*reinterpret_cast<const bf16x8 *>(sh.k + (16 * si[u] + j) * SH::KP + 4 * g4 + 64 * x),
+                               *reinterpret_cast<const bf16x8 *>(sh.q + (16 * ti[u] + j) * SH::QP + 4 * g4 + 64 * x),
+                               p[u]);
+            // ---- S^T q
             u32x2 qa[2][4], qb[2][4];
+            bf16x8 s[2][NC][2];
             auto read_q = [&](int x) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -339,123 +337,161 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
                     qb[x & 1][r] = *reinterpret_cast<const u32x2 *>(qp + 32);
                 }
             };
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int nc = 0; nc < NC; ++nc) o[r][nc] = f32x4{0, 0, 0, 0};
-            read_q(0);
-#pragma unroll
-            for (int x = 0; x < KT; ++x) {
-                __builtin_amdgcn_sched_barrier(0);
-                if (x + 1 < KT) read_q(x + 1);
-                bf16x8 s[2][NC];
+            auto split_state = [&](int x) {
 #pragma unroll
                 for (int nc = 0; nc < NC; ++nc) {
                     float f[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) f[i] = S[nc][2 * x][i], f[4 + i] = S[nc][2 * x + 1][i];
-                    s[0][nc] = take_part(f);
-                    s[1][nc] = take_part(f);
-                }
+                    s[x & 1][nc][0] = take_part(f);
+                    s[x & 1][nc][1] = take_part(f);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                    for (int i = 0; i < 4; ++i) S[nc][2 * x][i] *= keep, S[nc][2 * x + 1][i] *= keep;
+                }
+            };
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int nc = 0; nc < NC; ++nc) o[r][nc] = f32x4{0, 0, 0, 0};
+            read_q(0);
+            split_state(0);
+#pragma unroll
+            for (int x = 0; x < KT; ++x) {
+                __builtin_amdgcn_sched_barrier(0);
+                fetch(gk, k_step, a.dk, rk, x, next, place);
+                if (x + 1 < KT) read_q(x + 1);
+                if (x >= KT - NC) {
+                    read_for_decay(0, x - KT + NC);
+                    decay_v(0, x - KT + NC);
+                }
+                if (x + 1 < KT) split_state(x + 1);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
 #pragma unroll
                         for (int nc = 0; nc < NC; ++nc)
-                            o[r][nc] = mma(s[part][nc], frag(qa[x & 1][r], qb[x & 1][r]), o[r][nc]);
+                            o[r][nc] = mma(s[x & 1][nc][u], frag(qa[x & 1][r], qb[x & 1][r]), o[r][nc]);
+                in_turn<8 * NC, 4>();
             }
             __builtin_amdgcn_sched_barrier(0);
+            __syncthreads();                       // q has been used: the products take its place
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float e = dec.in[16 * r + j];
-#pragma unroll
-                for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[r][nc][i] *= e;
-            }
-            __syncthreads();                       // the products are there
-        }
-        if (t0 + C < n) fetch(n - t0 - C, place);
-
-        // ---- the state's update
-        bf16x8 vf[NC][2];
-        const float keep = dec.total;
-#pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[nc][d][i] *= keep;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            __builtin_amdgcn_sched_barrier(0);
-            const int t = 32 * x + 2 * g4 + j / 4;  // this lane's row of the transposing reads
-            float left[8];
-            load_vec<8>(dec.left + 32 * x + 2 * g4, left);
-            bf16x8 part[NC][PARTS];
+            for (int x = 0; x < KT; ++x) fetch(gk, k_step, a.dk, rk, x, next, place);
 #pragma unroll
             for (int nc = 0; nc < NC; ++nc) {
-                const int c = NC == 2 ? colw + 8 * (j % 4) + 4 * nc : colw + 4 * (j % 4);
-                const char *vp = sh.v + t * SH::VP + 2 * c;
-                vf[nc][x] = frag(read_transposed(vp), read_transposed(vp + 4 * SH::VP));
-                const u32x4 w = __builtin_bit_cast(u32x4, vf[nc][x]);
-                float f[8];
+                read_for_decay(0, nc);
+                decay_v(0, nc);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[2 * i] = bf16_lo(w[i]) * left[2 * i];
-                    f[2 * i + 1] = bf16_hi(w[i]) * left[2 * i + 1];
-                }
+                for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int u = 0; u < PARTS; ++u) part[nc][u] = take_part(f);
-            }
-            const char *kp = sh.k + t * SH::KP + 8 * (j % 4);
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const bf16x8 kf = frag(read_transposed(kp + 32 * d), read_transposed(kp + 32 * d + 4 * SH::KP));
-#pragma unroll
-                for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-                    for (int u = 0; u < PARTS; ++u) S[nc][d] = mma(kf, part[nc][u], S[nc][d]);
+                    for (int i = 0; i < 4; ++i) S[nc][d][i] *= keep;
             }
         }
 
-        if constexpr (OUT) {
-            // ---- the chunk's own tokens.  A v that is not finite makes its column of the state
-            // so (0 * inf is NaN): then such values are taken out, for a masked product of 0 must
-            // not carry them to the tokens before theirs, and what they reach is marked instead.
+        auto decay_products = [&](int u) {
+            const int t = 16 * ti[u] + j, s = 16 * si[u] + g4;
+            const float thi = dec.hi[t], tlo = dec.lo[t];
+            const f32x4 shi = *reinterpret_cast<const f32x4 *>(dec.hi + s);
+            const f32x4 slo = *reinterpret_cast<const f32x4 *>(dec.lo + s);
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i]));
+                float x = a.scale * p[u][i] * e;
+                asm("" : "+v"(x));                 // a select, not a branch round the products
+                f[i] = s + i <= t ? x : 0.0f;
+            }
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                const u32x2 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+                *reinterpret_cast<u32x2 *>(sh.p[part] + t * SH::PP + 2 * s) = w;
+                f[0] -= bf16_lo(w[0]), f[1] -= bf16_hi(w[0]);
+                f[2] -= bf16_lo(w[1]), f[3] -= bf16_hi(w[1]);
+            }
+        };
+        // ---- the state's update, two row tiles a step
+        bf16x8 kf[2][2];
+        auto read_k = [&](int step) {
+            const char *kp = sh.k + (32 * (step / KT) + 2 * g4 + j / 4) * SH::KP + 8 * (j % 4) + 64 * (step % KT);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                kf[step & 1][e] = frag(read_transposed(kp + 32 * e), read_transposed(kp + 32 * e + 4 * SH::KP));
+        };
+        read_k(0);
+        read_for_decay(1, 0);
+#pragma unroll
+        for (int step = 0; step < 2 * KT; ++step) {
             __builtin_amdgcn_sched_barrier(0);
+            if (step < U * VB) fetch(gv, v_step, dv_here, rv, step, next, place);
+            if constexpr (OUT)
+                if (step >= KT) fetch(gq, q_step, a.dk, rq, step - KT, next, place);
+            if (step + 1 < 2 * KT) read_k(step + 1);
+            if (step < NC) {
+                decay_v(1, step);
+                if (step + 1 < NC) read_for_decay(1, step + 1);
+            }
+            if constexpr (OUT) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (step == (NC + 1 + r < 2 * KT ? NC + 1 + r : 2 * KT - 1)) {
+                        const float e = dec.in[16 * r + j];
+#pragma unroll
+                        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[r][nc][i] *= e;
+                    }
+                if (step == NC - 1) decay_products(0);
+            }
+#pragma unroll
+            for (int u = 0; u < PARTS; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc)
+                        S[nc][2 * (step % KT) + e] = mma(kf[step & 1][e], part[step / KT][nc][u], S[nc][2 * (step % KT) + e]);
+            in_turn<2 * NC * PARTS, 4>();
+            if (step == NC) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (wave == W - 1) {
+                    if (more) scan(sh.d[turn ^ 1]);
+                } else if constexpr (OUT) {
+                    decay_products(1);
+                    decay_products(2);
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+
+        bf16x8 vf[NC][2];
+        if constexpr (OUT) {
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) vf[nc][x] = read_v(nc, x, j);
+        }
+        // A v that is not finite makes its column of the state so (0 * inf is NaN): then such
+        // values are taken out of the chunk's own products, for a masked product of 0 must not
+        // carry them to the tokens before theirs, and what they reach is marked instead.
+        bool any_bad = false;
+        uint32_t marks[OUT ? NC : 1] = {};         // bit 4 * r + i: output o[r][nc][i]
+        if constexpr (OUT) {
             bool bad = false;
 #pragma unroll
             for (int nc = 0; nc < NC; ++nc) bad |= !(__builtin_fabsf(S[nc][0][0]) < INFINITY);
-            const bool any_bad = __any(bad);
-            bf16x8 bf[NC][2];
-            if (any_bad) {
-                asm volatile("");                  // not to be computed where it is not needed
-#pragma unroll
-                for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) bf[nc][x] = take_bad(vf[nc][x]);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int x = 0; x <= r / 2; ++x)
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        const bf16x8 pf = *reinterpret_cast<const bf16x8 *>(
-                            sh.p[part] + (16 * r + j) * SH::PP + 64 * x + 4 * g4);
-#pragma unroll
-                        for (int nc = 0; nc < NC; ++nc) o[r][nc] = mma(vf[nc][x], pf, o[r][nc]);
-                    }
+            any_bad = __any(bad);
             if (any_bad) {
                 int token = j;                     // hidden: these masks are not worth registers
                 asm volatile("" : "+v"(token));
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+                for (int nc = 0; nc < NC; ++nc) {
+                    bf16x8 bf[2];
 #pragma unroll
-                    for (int nc = 0; nc < NC; ++nc) {
-                        f32x4 marks = {0, 0, 0, 0};
+                    for (int x = 0; x < 2; ++x) bf[x] = take_bad(vf[nc][x]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        f32x4 reached = {0, 0, 0, 0};
 #pragma unroll
                         for (int x = 0; x <= r / 2; ++x) {
                             u32x4 below;           // 1 where token s <= t
@@ -464,13 +500,41 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
                                 const int s = 32 * x + 2 * g4 + 2 * i, t = 16 * r + token;
                                 below[i] = (s <= t ? 0x3F80u : 0u) | (s + 1 <= t ? 0x3F800000u : 0u);
                             }
-                            marks = mma(bf[nc][x], __builtin_bit_cast(bf16x8, below), marks);
+                            reached = mma(bf[x], __builtin_bit_cast(bf16x8, below), reached);
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (marks[i] > 0.0f) o[r][nc][i] = NAN;
+                            if (reached[i] > 0.0f) marks[nc] |= 1u << (4 * r + i);
                     }
+                }
             }
+        }
+        __syncthreads();                           // the products are there, k and v have been used
+        stage(sh.k, SH::KP, a.dk, rk, next, place);
+        stage(sh.v, SH::VP, dv_here, rv, next, place);
+        if constexpr (OUT) {
+            // ---- the chunk's own tokens
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 2 * x; r < 4; ++r) {
+                        const char *pp = sh.p[u] + (16 * r + j) * SH::PP + 64 * x + 4 * g4;
+                        // the tile above the diagonal is not stored
+                        if (r == 2 * x) pp = g4 >= 8 ? sh.zeros : pp;
+                        const bf16x8 pf = *reinterpret_cast<const bf16x8 *>(pp);
+#pragma unroll
+                        for (int nc = 0; nc < NC; ++nc) o[r][nc] = mma(vf[nc][x], pf, o[r][nc]);
+                    }
+            if (any_bad)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (marks[nc] >> (4 * r + i) & 1) o[r][nc][i] = NAN;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float f[4 * NC];
@@ -480,10 +544,11 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
                     for (int i = 0; i < 4; ++i) f[4 * nc + i] = o[r][nc][i];
                 const int t = 16 * r + j, c = colw + NC * g4;
                 if (t0 + t < n && col0 + c < a.dv)
-                    store_vec<4 * NC>(out + (int64_t)(first + t0 + t) * a.o_tok + c, f);
+                    store_vec<4 * NC>(reinterpret_cast<Bf16 *>(out + (t * o_step + 2 * c)), f);
             }
+            out += (int64_t)C * o_step;
+            __syncthreads();                       // the products have been used: q takes their place
         }
-        __syncthreads();                           // every wavefront is done with the tiles
     }
 
     if constexpr (OUT) {
@@ -494,7 +559,7 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * d + g4 + i, c = col0 + column(nc);
+                    const int r = 16 * d + g4 + i, c = col0 + column(nc, j);
                     if (r < a.dk && c < a.dv) store_one(state + (int64_t)r * a.dv + c, S[nc][d][i]);
                 }
     } else {
@@ -502,35 +567,68 @@ __global__ __launch_bounds__(256, KT <= 4 ? 2 : 1) void chunked(const AttnArgs a
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-            for (int d = 0; d < DT; ++d) w[(nc * DT + d) * 256] = S[nc][d];
-        if (tid == 192) a.ws_total[ws_head] = __builtin_amdgcn_exp2f((float)whole);
+            for (int d = 0; d < DT; ++d) w[(nc * DT + d) * 64 * W] = S[nc][d];
+        if (tid == 64 * (W - 1)) a.ws_total[ws_head] = __builtin_amdgcn_exp2f((float)whole);
+    }
+}
+
+// Between the two: each segment's place in the workspace, which holds what its own tokens leave, is
+// left with what all of the row's up to it leave.  A workgroup has 256 vectors of one (row, v head,
+// tile), far apart from segment to segment; eight segments' are in flight at once.
+__global__ __launch_bounds__(64 * W) void combine(const AttnArgs a, const int vectors) {
+    const int parts = vectors / (64 * W);
+    int rest = blockIdx.x;
+    const int part = rest % parts;
+    rest /= parts;
+    const int ht = rest % (a.v_heads * a.tiles), i = rest / (a.v_heads * a.tiles);
+    const int count = uniform(segments_of(a, i));
+    if (count < 2) return;                         // same for the workgroup
+    const int64_t id = first_segment<W>(a, i);
+    if (id + count > a.segments) return;
+    const int64_t step = (int64_t)a.v_heads * a.tiles, at = id * step + ht;
+    f32x4 *w = static_cast<f32x4 *>(a.ws) + at * vectors + part * (64 * W) + threadIdx.x;
+    const float *total = a.ws_total + at;
+    f32x4 S = {0, 0, 0, 0};
+    constexpr int AHEAD = 8;
+    for (int s0 = 0; s0 < count - 1; s0 += AHEAD) {
+        f32x4 x[AHEAD];
+        float keep[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int s = s0 + u < count - 1 ? s0 + u : count - 2;
+            x[u] = w[s * step * vectors];
+            keep[u] = total[s * step];
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (s0 + u < count - 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[e] = fmaf(S[e], keep[u], x[u][e]);
+                w[(s0 + u) * step * vectors] = S;
+            }
     }
 }
 
 template <int KT, int NC, typename ST>
 ChunkedPlan plan() {
-    return {(const void *)chunked<KT, NC, ST, true>, (const void *)chunked<KT, NC, ST, false>, 64 * NC,
-            (int64_t)256 * NC * 2 * KT * 16};
+    return {(const void *)chunked<KT, NC, ST, true>, (const void *)chunked<KT, NC, ST, false>,
+            (const void *)combine, 16 * W * NC, 64 * W,
+            (int64_t)64 * W * NC * 2 * KT * 16};
 }
 
-template <typename ST>
-ChunkedPlan pick(int dk, int dv) {
-    if (dv <= 64) {
-        if (dk <= 64) return plan<2, 1, ST>();
-        if (dk <= 128) return plan<4, 1, ST>();
-        if (dk <= 192) return plan<6, 1, ST>();
-        return plan<8, 1, ST>();
-    }
-    if (dk <= 64) return plan<2, 2, ST>();
-    if (dk <= 128) return plan<4, 2, ST>();
-    if (dk <= 192) return plan<6, 2, ST>();
-    return plan<8, 2, ST>();
+template <int NC, typename ST>
+ChunkedPlan pick_for(int dk) {
+    if (dk <= 64) return plan<2, NC, ST>();
+    if (dk <= 128) return plan<4, NC, ST>();
+    if (dk <= 192) return plan<6, NC, ST>();
+    return plan<8, NC, ST>();
 }
 
 }  // namespace
 
-ChunkedPlan pick_chunked(int state_bytes, int dk, int dv) {
-    return state_bytes == 4 ? pick<float>(dk, dv) : pick<Bf16>(dk, dv);
+ChunkedPlan pick_chunked(int state_bytes, int dk, bool wide) {
+    if (state_bytes == 4) return wide ? pick_for<2, float>(dk) : pick_for<1, float>(dk);
+    return wide ? pick_for<2, Bf16>(dk) : pick_for<1, Bf16>(dk);
 }
 
 }  // namespace laimpl

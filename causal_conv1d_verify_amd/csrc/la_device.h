@@ -80,11 +80,21 @@ __device__ __forceinline__ void store_vec(Bf16 *p, const float (&f)[N]) {
 // differences of sums of decays stay defined; NaN stays NaN.
 __device__ __forceinline__ float finite_decay(float g) { return g < -1e6f ? -1e6f : g; }
 
+// A value that is the same in every lane, for the compiler to keep in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = (uint32_t)uniform((int)(uint32_t)x), hi = (uint32_t)uniform((int)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // One row of a batch: its token count (-1: skip the row), its slot and its first elements.
 struct Row {
     int n;
     int64_t slot, q, k, v, o, g;
 };
+__device__ __forceinline__ Row uniform(const Row &r) {
+    return Row{uniform(r.n), uniform(r.slot), uniform(r.q), uniform(r.k), uniform(r.v), uniform(r.o), uniform(r.g)};
+}
 __device__ __forceinline__ Row row_of(const AttnArgs &a, int i) {
     Row r;
     r.slot = a.slot_idx ? a.slot_idx[i] : i;
@@ -118,19 +128,20 @@ __device__ __forceinline__ void store_one(Bf16 *p, float x) {
 // Segment `id` of the rows in order, each row cut into ceil(tokens / seg_len) of them and one
 // where it has no tokens; row -1 where there are fewer.  Rows that are skipped have none, nor
 // has a row that would end past a.segments (more tokens than the caller declared).  Called by
-// a whole workgroup of 256, `shared` is two words of LDS.
+// a whole workgroup of W wavefronts, `shared` is two words of LDS.
 struct Segment { int row, index; bool last; };
 __device__ __forceinline__ int segments_of(const AttnArgs &a, int i) {
     const Row r = row_of(a, i);
     return r.n < 0 ? 0 : r.n == 0 ? 1 : (int)(((int64_t)r.n + a.seg_len - 1) / a.seg_len);
 }
+template <int W>
 __device__ __forceinline__ Segment find_segment(const AttnArgs &a, int id, int64_t *shared) {
     if (a.seg_len >= a.T) return row_of(a, id).n < 0 ? Segment{-1, 0, true} : Segment{id, 0, true};
-    __shared__ int sums[4];
+    __shared__ int sums[W];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t before = 0;                            // segments of the rows before these 256
+    int64_t before = 0;                            // segments of the rows before these
     if (threadIdx.x == 0) shared[0] = -1;
-    for (int i0 = 0; i0 < a.n_seq && before <= id; i0 += 256) {
+    for (int i0 = 0; i0 < a.n_seq && before <= id; i0 += 64 * W) {
         const int i = i0 + threadIdx.x;
         const int own = i < a.n_seq ? segments_of(a, i) : 0;
         int upto = own;
@@ -148,10 +159,27 @@ __device__ __forceinline__ Segment find_segment(const AttnArgs &a, int id, int64
             shared[0] = i;
             shared[1] = (id - at) * 2 + (id - at == own - 1);
         }
-        for (int w = 0; w < 4; ++w) before += sums[w];
+        for (int w = 0; w < W; ++w) before += sums[w];
     }
     __syncthreads();
-    return Segment{(int)shared[0], (int)(shared[1] >> 1), (shared[1] & 1) != 0};
+    const int64_t at = uniform(shared[1]);
+    return Segment{uniform((int)shared[0]), (int)(at >> 1), (at & 1) != 0};
+}
+
+// The number of row i's first segment (i the same for the workgroup).
+template <int W>
+__device__ __forceinline__ int64_t first_segment(const AttnArgs &a, int i) {
+    __shared__ int64_t sums[W];
+    int64_t own = 0;
+    for (int r = threadIdx.x; r < i; r += 64 * W) own += segments_of(a, r);
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d /= 2) own += __shfl_xor(own, d);
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = own;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) all += sums[w];
+    return uniform(all);
 }
 
 }  // namespace

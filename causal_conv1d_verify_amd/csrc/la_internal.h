@@ -53,14 +53,15 @@ struct RecurrentPlan {
 // wide: 16 lanes across the state's columns (64 fp32 / 128 bf16 columns a workgroup), else 8.
 RecurrentPlan pick_recurrent(int x_bytes, int state_bytes, int dk, bool wide);
 
-// Prompts in chunks.  `first` leaves what a segment adds to a state in the workspace, `run`
-// makes the outputs and the last state.
+// Prompts in chunks.  Where rows are cut, `first` leaves what each segment's tokens add to a state
+// in the workspace and `combine` adds up those of a row; `run` makes the outputs and the last state.
 struct ChunkedPlan {
-    const void *run, *first;
-    int cols;                     // columns of the state per workgroup of 256 lanes
+    const void *run, *first, *combine;
+    int cols, threads;            // columns of the state per workgroup
     int64_t ws_bytes;             // of one workgroup's state
 };
-ChunkedPlan pick_chunked(int state_bytes, int dk, int dv);
+// wide: 128 columns per workgroup, else 64.
+ChunkedPlan pick_chunked(int state_bytes, int dk, bool wide);
 
 struct NormPlan {
     const void *fn;
