@@ -1,5 +1,5 @@
-"""Builds libconvverify.so and liblinattn.so (HIP kernels for gfx950 + their C ABIs) in-tree
-with hipcc.
+"""Builds libconvverify.so and liblinattn.so (HIP kernels for gfx950 + their C ABIs) and the call
+module _lacall.so in-tree with hipcc.
 
 Usage: python -m causal_conv1d_verify_amd.build   (or __graft_entry__.build())
 """
@@ -22,6 +22,8 @@ LIB = os.path.join(PKG, "libconvverify.so")
 LIB_WC = os.path.join(PKG, "libconvverify_wc.so")
 # Linear attention and the norms behind the conv: a library of its own, with its own C ABI.
 LIB_LA = os.path.join(PKG, "liblinattn.so")
+# torch tensors to liblinattn.so in C (linear_attention.py has the same in Python).
+LIB_CALL = os.path.join(PKG, "_lacall.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -57,6 +59,22 @@ SOURCES_LA = [
     (f"la_{name}.hip", f"la_{name}", [f"--offload-arch={ARCH}", *DEVICE_FLAGS])
     for name in ("chunked", "recurrent", "norm")
 ] + [("la_api.cpp", "la_api", [])]
+
+
+def _call_module():
+    """The compile flags and the link flags of the call module: Python's and torch's."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    return ([f"-I{sysconfig.get_paths()['include']}", f"-isystem{root}/include",
+             f"-isystem{root}/include/torch/csrc/api/include", "-DUSE_ROCM",
+             "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"],
+            [f"-L{PKG}", "-llinattn", "-Wl,-rpath,$ORIGIN", f"-L{root}/lib", "-lc10", "-lc10_hip",
+             "-ltorch_cpu", "-ltorch_python"])
+
+
 MAX_JOBS = max(1, min(len(SOURCES) + len(SOURCES_WC) + len(SOURCES_LA), int(os.environ.get("MAX_JOBS", os.cpu_count() or 4))))
 
 
@@ -69,8 +87,8 @@ def _run(cmd):
 
 
 def build(verbose: bool = True) -> str:
-    """Builds libconvverify.so, the write-count test library libconvverify_wc.so and
-    liblinattn.so."""
+    """Builds libconvverify.so, the write-count test library libconvverify_wc.so, liblinattn.so
+    and _lacall.so."""
     os.makedirs(os.path.join(BUILD, "wc"), exist_ok=True)
     t0 = time.time()
     pending = []
@@ -81,7 +99,11 @@ def build(verbose: bool = True) -> str:
             obj = os.path.join(BUILD, stem + ".o")
             pending.append([HIPCC, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
             objs.append(obj)
-        libs.append((lib, objs))
+        libs.append((lib, objs, []))
+    compile_call, link_call = _call_module()
+    call_obj = os.path.join(BUILD, "la_call.o")
+    pending.insert(0, [HIPCC, *COMMON, *compile_call, "-c", os.path.join(CSRC, "la_call.cpp"), "-o", call_obj])
+    libs.append((LIB_CALL, [call_obj], link_call))
     running = []
 
     def reap(cmd, p):
@@ -102,12 +124,12 @@ def build(verbose: bool = True) -> str:
                                                   stderr=subprocess.PIPE, text=True)))
         cmd, p = running.pop(0)
         reap(cmd, p)
-    for lib, objs in libs:
+    for lib, objs, link in libs:
         tmp = lib + ".tmp"
-        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp])
+        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, *link, "-o", tmp])
         os.replace(tmp, lib)
     if verbose:
-        print(f"built {LIB}, {LIB_WC} and {LIB_LA} in {time.time() - t0:.1f}s", file=sys.stderr)
+        print(f"built {LIB}, {LIB_WC}, {LIB_LA} and {LIB_CALL} in {time.time() - t0:.1f}s", file=sys.stderr)
     return LIB
 
 

@@ -267,12 +267,38 @@ def _issue(lib, dev, fn, args, keep):
         raise LinAttnError(rc, _linattn.error_message(lib, rc))
 
 
+_call = None
+
+
+def _short():
+    """The call module (csrc/la_call.cpp): the same marshalling in C for calls that are plainly in
+    order; it answers None to all others, and they take the way above."""
+    global _call
+    if _call is None:
+        import torch  # noqa: F401  (its libraries, which the module is linked to)
+
+        from . import _lacall as _call
+    return _call
+
+
+def _done(rc) -> bool:
+    """Whether the call module took a call; raises on its error code."""
+    if rc is None:
+        return False
+    if rc == _lib.CV_OK:
+        return True
+    raise LinAttnError(rc, _linattn.error_message(_linattn.load(), rc))
+
+
 def linear_attn_prefill(q, k, v, g, state, out, cu_seqlens, *, max_len: int, scale=None,
                         slot_idx=None, has_initial_state=None, workspace=None,
                         stream=None) -> None:
     """Enqueue linear attention over packed prompts; each row's last state is left in its slot.
     max_len >= the longest prompt.  scale: dk ** -0.5 if None.  workspace: a uint8 tensor of
     at least the size that the shape needs (allocated here if None)."""
+    if stream is None and _done(_short().attn(0, q, k, v, g, state, out, cu_seqlens, max_len, scale,
+                                              slot_idx, has_initial_state, None, workspace)):
+        return
     _issue(*_attn_args("prefill", q, k, v, g, state, out, cu_seqlens=cu_seqlens, max_len=max_len,
                        scale=scale, slot_idx=slot_idx, has_initial_state=has_initial_state,
                        workspace=workspace, stream=stream))
@@ -280,12 +306,18 @@ def linear_attn_prefill(q, k, v, g, state, out, cu_seqlens, *, max_len: int, sca
 
 def linear_attn_update(q, k, v, g, state, out, *, scale=None, slot_idx=None, stream=None) -> None:
     """Enqueue T (1..32) new tokens of each row: out for each, and the state after the last."""
+    if stream is None and _done(_short().attn(1, q, k, v, g, state, out, None, None, scale, slot_idx,
+                                              None, None, None)):
+        return
     _issue(*_attn_args("update", q, k, v, g, state, out, scale=scale, slot_idx=slot_idx,
                        stream=stream))
 
 
 def linear_attn_verify(q, k, v, g, state, out, *, scale=None, slot_idx=None, stream=None) -> None:
     """Enqueue the outputs of T (1..32) draft tokens of each row; the state is only read."""
+    if stream is None and _done(_short().attn(2, q, k, v, g, state, out, None, None, scale, slot_idx,
+                                              None, None, None)):
+        return
     _issue(*_attn_args("verify", q, k, v, g, state, out, scale=scale, slot_idx=slot_idx,
                        stream=stream))
 
@@ -293,6 +325,9 @@ def linear_attn_verify(q, k, v, g, state, out, *, scale=None, slot_idx=None, str
 def linear_attn_commit(k, v, g, state, num_tokens=None, *, slot_idx=None, stream=None) -> None:
     """Enqueue the commit of the first num_tokens[i] (None: all) tokens of each row to its
     state."""
+    if stream is None and _done(_short().attn(3, None, k, v, g, state, None, None, None, None,
+                                              slot_idx, None, num_tokens, None)):
+        return
     _issue(*_attn_args("commit", None, k, v, g, state, None, num_tokens=num_tokens,
                        slot_idx=slot_idx, stream=stream))
 
@@ -302,6 +337,10 @@ def gated_norm(y, gate, weight, out, *, eps: float = 1e-6, activation: str = "si
     """Enqueue out = norm(y) * act(gate), or norm(y * act(gate)) with gate_first, the RMS norm
     (times weight) over the last dimension of y [rows, heads, dim] or [rows, dim].  gate may be
     None, out may be y."""
+    act = ACTIVATIONS.get(activation)
+    if stream is None and act is not None and _done(
+            _short().gated(y, gate, weight, out, eps, act, gate_first)):
+        return
     _issue(*_gated_args(y, gate, weight, out, eps=eps, activation=activation,
                         gate_first=gate_first, stream=stream))
 
@@ -311,6 +350,9 @@ def residual_norm(y, residual, pre_weight, out, *, post_weight=None, gate=None,
     """Enqueue a block's end: r = residual + scale * gate * norm(y) (norm with post_weight only,
     gate [rows, dim], [dim] or None) to residual_out (in place if None), and out = norm(r) with
     pre_weight, the next block's input (out and pre_weight may both be None)."""
+    if stream is None and _done(_short().residual(y, residual, pre_weight, out, post_weight, gate,
+                                                  scale, residual_out, eps)):
+        return
     _issue(*_residual_args(y, residual, pre_weight, out, post_weight=post_weight, gate=gate,
                            scale=scale, residual_out=residual_out, eps=eps, stream=stream))
 
