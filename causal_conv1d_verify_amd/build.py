@@ -57,7 +57,7 @@ SOURCES_WC = [
      ("cv_api.cpp", "wc/cv_api", ["-DCV_WRITE_COUNT"])]
 SOURCES_LA = [
     (f"la_{name}.hip", f"la_{name}", [f"--offload-arch={ARCH}", *DEVICE_FLAGS])
-    for name in ("chunked", "recurrent", "norm")
+    for name in ("chunked", "chunked_f32", "few", "recurrent", "norm")
 ] + [("la_api.cpp", "la_api", [])]
 
 

@@ -167,7 +167,7 @@ int recurrent(laimpl::AttnArgs a, int xb, int sb, void *stream) {
     return launch(p.fn, heads * a.tiles, p.threads, 0, &a, stream);
 }
 
-// How packed prompts of bf16 tokens are cut into workgroups.
+// How packed prompts are cut into workgroups.
 //
 // Along a row: its tokens are one chain of chunks in one workgroup unless that chain is much
 // longer than the share of all chunks that each of the chip's slots would have (two workgroups on
@@ -175,7 +175,7 @@ int recurrent(laimpl::AttnArgs a, int xb, int sb, void *stream) {
 // of passing over their k and v twice (one prompt of 16384 with 32 heads: 202 us in 16
 // segments).
 //
-// Across a head: tiles of 128 columns, since what a chunk reads and the products q.k serve all of
+// Across a head (bf16 tokens; fp32 ones go in tiles of 64): tiles of 128 columns, since what a chunk reads and the products q.k serve all of
 // a tile; tiles of 64 where the wide ones would leave most compute units empty (64 workgroups of
 // 32 chunks: 122 us for 160).
 struct Cut {
@@ -183,36 +183,37 @@ struct Cut {
     int64_t tiles, segments, ws_states, ws_bytes;
     int32_t seg_len;
 };
-Cut cut_prompts(const la_shape_t *s, int sb, bool wide) {
-    constexpr int64_t kChunk = 64, kSlots = 512, kLeast = 4;
+Cut cut_prompts(const la_shape_t *s, int xb, int sb, bool wide) {
+    constexpr int64_t kSlots = 512, kLeast = 4;
     Cut c{};
-    c.plan = laimpl::pick_chunked(sb, s->dk, wide);
+    c.plan = xb == 4 ? laimpl::pick_chunked_f32(s->dk) : laimpl::pick_chunked(sb, s->dk, wide);
+    const int64_t chunk = c.plan.chunk;
     c.tiles = (s->dv + c.plan.cols - 1) / c.plan.cols;
     c.segments = s->n_seq;
     c.seg_len = s->T;
     const int64_t heads = s->v_heads * c.tiles;
     int64_t tokens = sat_mul(s->n_seq, s->T);
     if (s->tokens > 0 && s->tokens < tokens) tokens = s->tokens;
-    const int64_t chain = (s->T + kChunk - 1) / kChunk;
-    const int64_t share = std::max(kLeast, sat_mul(tokens / kChunk + 1, heads) / kSlots);
-    const int64_t segments = tokens / (share * kChunk) + s->n_seq;
+    const int64_t chain = (s->T + chunk - 1) / chunk;
+    const int64_t share = std::max(kLeast, sat_mul(tokens / chunk + 1, heads) / kSlots);
+    const int64_t segments = tokens / (share * chunk) + s->n_seq;
     const int64_t states = sat_mul(segments, heads);
     if (chain > share + share / 2 && chain > 2 * kLeast && states <= INT32_MAX) {
-        c.seg_len = (int32_t)(share * kChunk);
+        c.seg_len = (int32_t)(share * chunk);
         c.segments = segments;
         c.ws_states = states;
         c.ws_bytes = sat_add(sat_mul(states, c.plan.ws_bytes), (4 * states + 15) / 16 * 16);
     }
-    if (wide && c.segments * heads <= 128) return cut_prompts(s, sb, false);
+    if (wide && c.segments * heads <= 128) return cut_prompts(s, xb, sb, false);
     return c;
 }
-Cut cut_prompts(const la_shape_t *s, int sb) { return cut_prompts(s, sb, s->dv > 64); }
+Cut cut_prompts(const la_shape_t *s, int xb, int sb) { return cut_prompts(s, xb, sb, xb == 2 && s->dv > 64); }
 
-// Whether prompts go in chunks: bf16 tokens whose chunk lies within 32-bit offsets.  (Tokens
-// 32 MiB and more apart go one by one.)
-bool in_chunks(const la_shape_t *s, int xb) {
+// Whether prompts go in chunks: a chunk lies within 32-bit offsets.  (Tokens 32 MiB and more apart
+// go one by one.)
+bool in_chunks(const la_shape_t *s) {
     const int64_t far = std::max(std::max(s->q_tok_stride, s->k_tok_stride), std::max(s->v_tok_stride, s->out_tok_stride));
-    return xb == 2 && far < (1 << 24);
+    return far < (1 << 24);
 }
 
 int chunked(laimpl::AttnArgs a, const Cut &c, void *workspace, void *stream) {
@@ -247,8 +248,14 @@ int few_tokens(const la_shape_t *s, const Need &need, const void *q, const void 
                           {"state", state, true, 16}, {"out", out, need.out, 16}, {"g", g, false, 4},
                           {"slot_idx", slot_idx, false, 4}, {"num_tokens", num_tokens, false, 4}};
     if ((rc = check_pointers(ps)) != CV_OK) return rc;
-    return recurrent(attn_args(s, q, k, v, g, state, slot_idx, nullptr, num_tokens, nullptr, out, !need.verify),
-                     xb, sb, stream);
+    laimpl::AttnArgs a = attn_args(s, q, k, v, g, state, slot_idx, nullptr, num_tokens, nullptr, out, !need.verify);
+    // On the matrix cores where tokens are bf16, single ones only where the state's traffic counts
+    // (256 rows of 32 heads: 184 us for 197); for few workgroups the recurrence starts sooner (one row
+    // of 48 heads: 4.4 us for 6.5).
+    a.tiles = (s->dv + 127) / 128;
+    const int64_t blocks = (int64_t)s->n_seq * s->v_heads * a.tiles;
+    if (xb == 4 || (s->T == 1 && blocks < kWideBlocks)) return recurrent(a, xb, sb, stream);
+    return launch(laimpl::pick_few(sb, s->dk, s->T, need.out, !need.verify), blocks, 256, 0, &a, stream);
 }
 
 int check_norm(const la_norm_shape_t *s, bool residual, int *xb, int *rb) {
@@ -292,8 +299,8 @@ int64_t linattn_prefill_workspace(const la_shape_t *s) {
     int xb, sb;
     bool empty;
     const int rc = check_attn(s, Need{true, true, true, false}, &xb, &sb, &empty);
-    if (rc != CV_OK || empty || !in_chunks(s, xb)) return rc;
-    return cut_prompts(s, sb).ws_bytes;
+    if (rc != CV_OK || empty || !in_chunks(s)) return rc;
+    return cut_prompts(s, xb, sb).ws_bytes;
 }
 
 int linattn_prefill(const la_shape_t *s, const void *q, const void *k, const void *v, const float *g, void *state,
@@ -314,8 +321,8 @@ int linattn_prefill(const la_shape_t *s, const void *q, const void *k, const voi
     if ((rc = check_pointers(ps)) != CV_OK) return rc;
     const int xb = dtype_bytes(s->x_dtype), sb = dtype_bytes(s->state_dtype);
     const laimpl::AttnArgs a = attn_args(s, q, k, v, g, state, slot_idx, cu_seqlens, nullptr, has_initial_state, out, true);
-    if (!in_chunks(s, xb)) return recurrent(a, xb, sb, hip_stream);
-    return chunked(a, cut_prompts(s, sb), workspace, hip_stream);
+    if (!in_chunks(s)) return recurrent(a, xb, sb, hip_stream);
+    return chunked(a, cut_prompts(s, xb, sb), workspace, hip_stream);
 }
 
 int linattn_update(const la_shape_t *s, const void *q, const void *k, const void *v, const float *g, void *state,

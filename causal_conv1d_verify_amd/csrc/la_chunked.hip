@@ -18,56 +18,12 @@
 // are stored as they come and read transposed where a product needs their tokens in a lane.
 #include <type_traits>
 
-#include "la_device.h"
+#include "la_matrix.h"
 
 namespace laimpl {
 namespace {
 
 constexpr int C = 64;              // tokens of a chunk: one per lane of the scan
-
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-
-// Row 4g + i (i = 0..3) of column j for lane (g, j), from 4 rows of 16 columns for each g: lane
-// (g, j) points at row 4g + j / 4, columns 4 * (j % 4) to + 3.
-__device__ __forceinline__ u32x2 read_transposed(const char *p) {
-    const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    return __builtin_bit_cast(u32x2, r);
-}
-
-__device__ __forceinline__ bf16x8 frag(u32x2 a, u32x2 b) {
-    const u32x4 w = {a[0], a[1], b[0], b[1]};
-    return __builtin_bit_cast(bf16x8, w);
-}
-
-__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-// The next bf16 part of eight values, taken off them.
-__device__ __forceinline__ bf16x8 take_part(float (&x)[8]) {
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        x[2 * i] -= bf16_lo(w[i]);
-        x[2 * i + 1] -= bf16_hi(w[i]);
-    }
-    return __builtin_bit_cast(bf16x8, w);
-}
-
-// Non-finite elements of eight bf16 values: zeroed in v, 1 in the returned indicator.
-__device__ __forceinline__ bf16x8 take_bad(bf16x8 &v) {
-    u32x4 w = __builtin_bit_cast(u32x4, v), bad;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = (w[i] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u;
-        const uint32_t hi = (w[i] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-        bad[i] = (lo & 0x3F80u) | (hi & 0x3F800000u);
-        w[i] &= ~(lo | hi);
-    }
-    v = __builtin_bit_cast(bf16x8, w);
-    return __builtin_bit_cast(bf16x8, bad);
-}
 
 // The vector work of a step between its M matrix instructions, V to each.
 template <int M, int V>
@@ -77,26 +33,6 @@ __device__ __forceinline__ void in_turn() {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // a matrix instruction
         __builtin_amdgcn_sched_group_barrier(0x002, V, 0);     // vector instructions
     }
-}
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double add_from(double x) {
-    const uint64_t w = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)w, CTRL, ROWS, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(w >> 32), CTRL, ROWS, 0xF, false);
-    return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-// The sum over the lanes up to each one, by data moves between lanes: inside rows of 16 from 1, 2,
-// 4 and 8 lanes before (zeros from outside), then row 0's to row 1 and 2's to 3, then 0 and 1's
-// to 2 and 3.
-__device__ __forceinline__ double running_sum(double x) {
-    x = add_from<0x111, 0xF>(x);
-    x = add_from<0x112, 0xF>(x);
-    x = add_from<0x114, 0xF>(x);
-    x = add_from<0x118, 0xF>(x);
-    x = add_from<0x142, 0xA>(x);
-    return add_from<0x143, 0xC>(x);
 }
 
 struct __attribute__((aligned(16))) Decays {   // of one chunk
@@ -612,7 +548,7 @@ __global__ __launch_bounds__(64 * W) void combine(const AttnArgs a, const int ve
 template <int KT, int NC, typename ST>
 ChunkedPlan plan() {
     return {(const void *)chunked<KT, NC, ST, true>, (const void *)chunked<KT, NC, ST, false>,
-            (const void *)combine, 16 * W * NC, 64 * W,
+            (const void *)combine, 16 * W * NC, 64 * W, C,
             (int64_t)64 * W * NC * 2 * KT * 16};
 }
 

@@ -57,11 +57,15 @@ RecurrentPlan pick_recurrent(int x_bytes, int state_bytes, int dk, bool wide);
 // in the workspace and `combine` adds up those of a row; `run` makes the outputs and the last state.
 struct ChunkedPlan {
     const void *run, *first, *combine;
-    int cols, threads;            // columns of the state per workgroup
+    int cols, threads, chunk;     // columns of the state per workgroup; tokens of a chunk
     int64_t ws_bytes;             // of one workgroup's state
 };
 // wide: 128 columns per workgroup, else 64.
 ChunkedPlan pick_chunked(int state_bytes, int dk, bool wide);
+ChunkedPlan pick_chunked_f32(int dk);        // fp32 tokens and state
+
+// Up to 32 tokens of bf16 in one pass over the state: 128 columns per workgroup of 256 lanes.
+const void *pick_few(int state_bytes, int dk, int T, bool out, bool write);
 
 struct NormPlan {
     const void *fn;
