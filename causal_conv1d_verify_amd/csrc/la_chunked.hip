@@ -25,16 +25,6 @@ namespace {
 
 constexpr int C = 64;              // tokens of a chunk: one per lane of the scan
 
-// The vector work of a step between its M matrix instructions, V to each.
-template <int M, int V>
-__device__ __forceinline__ void in_turn() {
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // a matrix instruction
-        __builtin_amdgcn_sched_group_barrier(0x002, V, 0);     // vector instructions
-    }
-}
-
 struct __attribute__((aligned(16))) Decays {   // of one chunk
     float hi[C], lo[C];            // running sums in base 2, as pairs
     float in[C], left[C];          // scale * 2^(sum up to t), 2^(sum behind t)
@@ -161,7 +151,8 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
     const float *gg = a.g ? a.g + row.g + h + (int64_t)first * a.g_tok : nullptr;
     float g_next = 0.0f;
     auto fetch_decays = [&](int t0) {
-        if (gg) g_next = t0 + lane < n ? gg[(int64_t)(t0 + lane) * a.g_tok] : 0.0f;
+        // a line for each token: by the wavefront that sums them only
+        if (wave == W - 1 && gg) g_next = t0 + lane < n ? gg[(int64_t)(t0 + lane) * a.g_tok] : 0.0f;
     };
     double whole = 0.0;                            // log2 of the segment's decay (that wavefront)
     auto scan = [&](Decays &d) {
@@ -195,15 +186,17 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
                     : nullptr;
     const uint32_t o_step = 2 * (uint32_t)a.o_tok;
 
-    // Each step below issues matrix instructions whose operands the step before it made, and
-    // between them the vector work and the reads that the next step needs: a wavefront issues in
-    // order, and there are few of them.
+    // Each step below issues matrix instructions whose operands the step before it made, beside the
+    // vector work and the reads that the next step needs: a wavefront issues in order, and there
+    // are few of them.  A step is closed to the scheduler, which would otherwise hold more of the
+    // next ones' operands than there are registers.
     for (int t0 = 0, turn = 0; t0 < n; t0 += C, turn ^= 1) {
         // The lane's place, hidden at each chunk: what is derived from it is computed again
         // rather than kept in registers, which are short here.
         int place = tid;
         asm volatile("" : "+v"(place));
         const int j = place & 15, g4 = (place & 48) >> 2;
+        const u32x2 minus = minus_identity(place & 63);
         // the next chunk (this one again behind the last: what is fetched then is not used)
         const bool more = n - t0 > C;
         const int next = more ? n - t0 - C : n - t0;
@@ -231,14 +224,18 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
         };
         auto decay_v = [&](int x, int nc) {
             const u32x4 w = __builtin_bit_cast(u32x4, raw);
-            float f[8];
+            f32x4 f[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                f[2 * i] = bf16_lo(w[i]) * left[2 * i];
-                f[2 * i + 1] = bf16_hi(w[i]) * left[2 * i + 1];
+                f[i / 2][i % 2 * 2] = bf16_lo(w[i]) * left[2 * i];
+                f[i / 2][i % 2 * 2 + 1] = bf16_hi(w[i]) * left[2 * i + 1];
             }
 #pragma unroll
-            for (int u = 0; u < PARTS; ++u) part[x][nc][u] = take_part(f);
+            for (int u = 0; u < PARTS; ++u) {
+                const u32x2 a = part_of(f[0]), b = part_of(f[1]);
+                part[x][nc][u] = frag(a, b);
+                if (u + 1 < PARTS) f[0] = less(f[0], a, minus), f[1] = less(f[1], b, minus);
+            }
         };
 
         f32x4 o[OUT ? 4 : 1][NC];                  // outputs, transposed: lane = token, 4 columns
@@ -276,11 +273,9 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
             auto split_state = [&](int x) {
 #pragma unroll
                 for (int nc = 0; nc < NC; ++nc) {
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = S[nc][2 * x][i], f[4 + i] = S[nc][2 * x + 1][i];
-                    s[x & 1][nc][0] = take_part(f);
-                    s[x & 1][nc][1] = take_part(f);
+                    const u32x2 a = part_of(S[nc][2 * x]), b = part_of(S[nc][2 * x + 1]);
+                    s[x & 1][nc][0] = frag(a, b);
+                    s[x & 1][nc][1] = frag(part_of(less(S[nc][2 * x], a, minus)), part_of(less(S[nc][2 * x + 1], b, minus)));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) S[nc][2 * x][i] *= keep, S[nc][2 * x + 1][i] *= keep;
                 }
@@ -308,7 +303,6 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
 #pragma unroll
                         for (int nc = 0; nc < NC; ++nc)
                             o[r][nc] = mma(s[x & 1][nc][u], frag(qa[x & 1][r], qb[x & 1][r]), o[r][nc]);
-                in_turn<8 * NC, 4>();
             }
             __builtin_amdgcn_sched_barrier(0);
             __syncthreads();                       // q has been used: the products take its place
@@ -331,7 +325,7 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
             const float thi = dec.hi[t], tlo = dec.lo[t];
             const f32x4 shi = *reinterpret_cast<const f32x4 *>(dec.hi + s);
             const f32x4 slo = *reinterpret_cast<const f32x4 *>(dec.lo + s);
-            float f[4];
+            f32x4 f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float e = __builtin_amdgcn_exp2f((thi - shi[i]) + (tlo - slo[i]));
@@ -341,10 +335,9 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
             }
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-                const u32x2 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+                const u32x2 w = part_of(f);
                 *reinterpret_cast<u32x2 *>(sh.p[part] + t * SH::PP + 2 * s) = w;
-                f[0] -= bf16_lo(w[0]), f[1] -= bf16_hi(w[0]);
-                f[2] -= bf16_lo(w[1]), f[3] -= bf16_hi(w[1]);
+                if (part == 0) f = less(f, w, minus);
             }
         };
         // ---- the state's update, two row tiles a step
@@ -387,7 +380,6 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
 #pragma unroll
                     for (int nc = 0; nc < NC; ++nc)
                         S[nc][2 * (step % KT) + e] = mma(kf[step & 1][e], part[step / KT][nc][u], S[nc][2 * (step % KT) + e]);
-            in_turn<2 * NC * PARTS, 4>();
             if (step == NC) {
                 __builtin_amdgcn_sched_barrier(0);
                 if (wave == W - 1) {
@@ -446,8 +438,6 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
             }
         }
         __syncthreads();                           // the products are there, k and v have been used
-        stage(sh.k, SH::KP, a.dk, rk, next, place);
-        stage(sh.v, SH::VP, dv_here, rv, next, place);
         if constexpr (OUT) {
             // ---- the chunk's own tokens
 #pragma unroll
@@ -463,6 +453,10 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
 #pragma unroll
                         for (int nc = 0; nc < NC; ++nc) o[r][nc] = mma(vf[nc][x], pf, o[r][nc]);
                     }
+        }
+        stage(sh.k, SH::KP, a.dk, rk, next, place);
+        stage(sh.v, SH::VP, dv_here, rv, next, place);
+        if constexpr (OUT) {
             if (any_bad)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)

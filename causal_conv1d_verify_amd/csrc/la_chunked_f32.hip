@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * W) void chunked_f32(const AttnArgs a) {
     };
     const float *gg = a.g ? a.g + row.g + h + (int64_t)first * a.g_tok : nullptr;
     float g_next = 0.0f;
-    auto fetch_decays = [&](int t0) { g_next = gg && lane < C && t0 + lane < n ? gg[(int64_t)(t0 + lane) * a.g_tok] : 0.0f; };
+    auto fetch_decays = [&](int t0) { g_next = gg && wave == W - 1 && lane < C && t0 + lane < n ? gg[(int64_t)(t0 + lane) * a.g_tok] : 0.0f; };
     double whole = 0.0;
     auto scan = [&](Decays32 &d) {
         const double x = running_sum(1.4426950408889634 * (double)finite_decay(g_next));

@@ -27,6 +27,19 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// Four 32-bit values to bf16, and what that leaves of them: x - part, exact.  In the order of a
+// result's registers the difference is a product with minus the identity (`minus`, of this lane),
+// which costs the wavefront one issue where the vector unit would take eight.
+__device__ __forceinline__ u32x2 part_of(f32x4 x) { return u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])}; }
+__device__ __forceinline__ u32x2 minus_identity(int lane) {
+    const uint32_t one = lane / 16 == lane % 16 / 4 ? 0xBF80u << 16 * (lane % 2) : 0u;
+    return lane & 2 ? u32x2{0, one} : u32x2{one, 0};
+}
+__device__ __forceinline__ f32x4 less(f32x4 x, u32x2 part, u32x2 minus) {
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, minus), __builtin_bit_cast(s16x4, part), x,
+                                                     0, 0, 0);
+}
+
 // The next bf16 part of eight values, taken off them.
 __device__ __forceinline__ bf16x8 take_part(float (&x)[8]) {
     u32x4 w;
