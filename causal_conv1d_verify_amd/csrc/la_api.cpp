@@ -133,6 +133,12 @@ int launch(const void *fn, int64_t blocks, int threads, int64_t lds, void *args,
     return CV_OK;
 }
 
+// What a call passes over and the 256 MiB Infinity Cache will hardly hold until it is read again (in
+// a model, behind every other layer's work).  From about 96 MiB on a state's loads and stores are
+// faster past the caches (256 rows of 2 MiB: 165 us for 184; 64 rows in turn with others: 54 for
+// 60), below they are not (16 rows: 18 us for 17).
+bool past_caches(int64_t bytes) { return bytes > (96 << 20); }
+
 laimpl::AttnArgs attn_args(const la_shape_t *s, const void *q, const void *k, const void *v, const float *g,
                            const void *state, const int32_t *slot_idx, const int32_t *cu,
                            const int32_t *num_tokens, const int32_t *has_init, void *out, bool write_state) {
@@ -254,6 +260,7 @@ int few_tokens(const la_shape_t *s, const Need &need, const void *q, const void 
     // of 48 heads: 4.4 us for 6.5).
     a.tiles = (s->dv + 127) / 128;
     const int64_t blocks = (int64_t)s->n_seq * s->v_heads * a.tiles;
+    a.streaming = past_caches(sat_mul((int64_t)s->n_seq * s->v_heads, (int64_t)s->dk * s->dv * sb));
     if (xb == 4 || (s->T == 1 && blocks < kWideBlocks)) return recurrent(a, xb, sb, stream);
     return launch(laimpl::pick_few(sb, s->dk, s->T, need.out, !need.verify), blocks, 256, 0, &a, stream);
 }

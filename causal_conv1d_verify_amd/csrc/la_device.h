@@ -28,50 +28,63 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// 4, 8 or 16 bytes; with STREAM past the caches' usual order, for what no cache can hold until it is
+// read again.
+template <bool STREAM, typename V>
+__device__ __forceinline__ V load_as(const void *p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const V *>(p));
+    else return *static_cast<const V *>(p);
+}
+template <bool STREAM, typename V>
+__device__ __forceinline__ void store_as(void *p, V x) {
+    if constexpr (STREAM) __builtin_nontemporal_store(x, static_cast<V *>(p));
+    else *static_cast<V *>(p) = x;
+}
+
 // N consecutive elements (N a multiple of 4 for float, 4 or a multiple of 8 for bf16) as floats.
-template <int N>
+template <int N, bool STREAM = false>
 __device__ __forceinline__ void load_vec(const float *p, float (&f)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-        const f32x4 w = *reinterpret_cast<const f32x4 *>(p + i);
+        const f32x4 w = load_as<STREAM, f32x4>(p + i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i + j] = w[j];
     }
 }
-template <int N>
+template <int N, bool STREAM = false>
 __device__ __forceinline__ void load_vec(const Bf16 *p, float (&f)[N]) {
     if constexpr (N == 4) {
-        const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+        const u32x2 w = load_as<STREAM, u32x2>(p);
 #pragma unroll
         for (int j = 0; j < 2; ++j) f[2 * j] = bf16_lo(w[j]), f[2 * j + 1] = bf16_hi(w[j]);
     } else {
 #pragma unroll
         for (int i = 0; i < N; i += 8) {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(p + i);
+            const u32x4 w = load_as<STREAM, u32x4>(p + i);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[i + 2 * j] = bf16_lo(w[j]), f[i + 2 * j + 1] = bf16_hi(w[j]);
         }
     }
 }
-template <int N>
+template <int N, bool STREAM = false>
 __device__ __forceinline__ void store_vec(float *p, const float (&f)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
         const f32x4 w = {f[i], f[i + 1], f[i + 2], f[i + 3]};
-        *reinterpret_cast<f32x4 *>(p + i) = w;
+        store_as<STREAM>(p + i, w);
     }
 }
-template <int N>
+template <int N, bool STREAM = false>
 __device__ __forceinline__ void store_vec(Bf16 *p, const float (&f)[N]) {
     if constexpr (N == 4) {
         const u32x2 w = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
-        *reinterpret_cast<u32x2 *>(p) = w;
+        store_as<STREAM>(p, w);
     } else {
 #pragma unroll
         for (int i = 0; i < N; i += 8) {
             const u32x4 w = {pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]),
                              pack_bf16(f[i + 4], f[i + 5]), pack_bf16(f[i + 6], f[i + 7])};
-            *reinterpret_cast<u32x4 *>(p + i) = w;
+            store_as<STREAM>(p + i, w);
         }
     }
 }

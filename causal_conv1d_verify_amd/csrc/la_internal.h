@@ -28,6 +28,7 @@ struct AttnArgs {
     int32_t dk, dv, n_slots, tiles;     // tiles = workgroups along dv of a head
     float scale;
     int32_t write_state;
+    int32_t streaming;            // the states of this call are more than the caches keep
     // prompts in chunks: a row is cut into segments of seg_len tokens (a multiple of the chunk;
     // rows of at most seg_len tokens are one)
     int32_t seg_len, segments;          // segments that the grid and the workspace hold
