@@ -87,9 +87,11 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
             if (!OUT || !init) continue;
             const int c = col0 + column(nc, j);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i) {          // loads without branches, the first place where there is none
                 const int r = 16 * d + g4 + i;
-                if (r < a.dk && c < a.dv) S[nc][d][i] = load_one(state + (int64_t)r * a.dv + c);
+                const bool in = r < a.dk && c < a.dv;
+                const float x = load_one(state + (in ? r * a.dv + c : 0));
+                S[nc][d][i] = in ? x : 0.0f;
             }
         }
     const int64_t ws_head = ((int64_t)id * a.v_heads + h) * a.tiles + tile;
@@ -483,15 +485,19 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
 
     if constexpr (OUT) {
         if (!seg.last) return;
+        auto store = [&](auto whole) {
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
+            for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
+                for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * d + g4 + i, c = col0 + column(nc, j);
-                    if (r < a.dk && c < a.dv) store_one(state + (int64_t)r * a.dv + c, S[nc][d][i]);
-                }
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * d + g4 + i, c = col0 + column(nc, j);
+                        if (decltype(whole)::value || (r < a.dk && c < a.dv)) store_one(state + (r * a.dv + c), S[nc][d][i]);
+                    }
+        };
+        if (whole_tile) store(std::true_type{});
+        else store(std::false_type{});
     } else {
         f32x4 *w = static_cast<f32x4 *>(a.ws) + ws_head * WS + tid;
 #pragma unroll

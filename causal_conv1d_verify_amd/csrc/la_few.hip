@@ -31,6 +31,9 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
     constexpr int SPARTS = sizeof(ST) == 4 ? 2 : 1;
     constexpr int KP = 128 * RB + 32;              // bytes of a token's k in LDS
     __shared__ __attribute__((aligned(16))) char sk[WRITE ? 16 * TT * KP : 16];
+    __shared__ struct __attribute__((aligned(16))) {       // each wavefront's own: it waits for no other's
+        float hi[4][32], lo[4][32], in[4][32], left[4][32];
+    } dec;
     __shared__ f32x4 half[OUT ? 2 * TT * NC * kWave : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -127,8 +130,13 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
     // ---- the decays, lane = token
     double sum = running_sum(1.4426950408889634 * (double)finite_decay(g));
     const double total = __shfl(sum, kWave - 1);
-    const float hi = (float)sum, lo = (float)(sum - hi);
-    const float left = __builtin_amdgcn_exp2f((float)(total - sum));
+    if (lane < 32) {
+        const float hi = (float)sum;
+        dec.hi[wave][lane] = hi;
+        dec.lo[wave][lane] = (float)(sum - hi);
+        dec.in[wave][lane] = a.scale * __builtin_amdgcn_exp2f(hi);
+        dec.left[wave][lane] = __builtin_amdgcn_exp2f((float)(total - sum));
+    }
 
     f32x4 o[OUT ? TT : 1][NC];
     if constexpr (OUT) {
@@ -165,8 +173,7 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
         const bool any_bad = __any(some != 0);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const float thi = __shfl(hi, 16 * t + j), tlo = __shfl(lo, 16 * t + j);
-            const float in = a.scale * __builtin_amdgcn_exp2f(thi);
+            const float thi = dec.hi[wave][16 * t + j], tlo = dec.lo[wave][16 * t + j], in = dec.in[wave][16 * t + j];
 #pragma unroll
             for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -178,10 +185,12 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
                 f32x4 p = {0, 0, 0, 0};            // transposed: lane = t
 #pragma unroll
                 for (int b = 0; b < RB; ++b) p = mma(kf[s][b], qf[t][b], p);
+                const f32x4 shi = *reinterpret_cast<const f32x4 *>(&dec.hi[wave][16 * s + g4]);
+                const f32x4 slo = *reinterpret_cast<const f32x4 *>(&dec.lo[wave][16 * s + g4]);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int at = 16 * s + g4 + u;
-                    const float e = __builtin_amdgcn_exp2f((thi - __shfl(hi, at)) + (tlo - __shfl(lo, at)));
+                    const float e = __builtin_amdgcn_exp2f((thi - shi[u]) + (tlo - slo[u]));
                     float x = a.scale * p[u] * e;
                     asm("" : "+v"(x));             // a select, not a branch round the products
                     const bool on = at <= 16 * t + j;
@@ -239,7 +248,7 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) by[4 * t + u] = t < TT ? __shfl(left, 16 * t + g4 + u) : 0.0f;
+            for (int u = 0; u < 4; ++u) by[4 * t + u] = t < TT ? dec.left[wave][16 * t + g4 + u] : 0.0f;
         bf16x8 part[NC][PARTS];
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
