@@ -183,14 +183,16 @@ int recurrent(laimpl::AttnArgs a, int xb, int sb, void *stream) {
 //
 // Across a head (bf16 tokens; fp32 ones go in tiles of 64): tiles of 128 columns, since what a chunk reads and the products q.k serve all of
 // a tile; tiles of 64 where the wide ones would leave most compute units empty (64 workgroups of
-// 32 chunks: 122 us for 160).
+// 32 chunks: 122 us for 160) or the state's way in and out counts, in a few chunks of one
+// generation of workgroups (8 rows of up to 160 tokens, 48 heads: 25 us for 27).
 struct Cut {
     laimpl::ChunkedPlan plan;
     int64_t tiles, segments, ws_states, ws_bytes;
     int32_t seg_len;
 };
 Cut cut_prompts(const la_shape_t *s, int xb, int sb, bool wide) {
-    constexpr int64_t kSlots = 512, kLeast = 4;
+    constexpr int64_t kSlots = 512;
+    constexpr int64_t kLeast = 4;
     Cut c{};
     c.plan = xb == 4 ? laimpl::pick_chunked_f32(s->dk) : laimpl::pick_chunked(sb, s->dk, wide);
     const int64_t chunk = c.plan.chunk;
@@ -210,7 +212,7 @@ Cut cut_prompts(const la_shape_t *s, int xb, int sb, bool wide) {
         c.ws_states = states;
         c.ws_bytes = sat_add(sat_mul(states, c.plan.ws_bytes), (4 * states + 15) / 16 * 16);
     }
-    if (wide && c.segments * heads <= 128) return cut_prompts(s, xb, sb, false);
+    if (wide && (c.segments * heads <= 128 || (chain <= 4 && c.segments * heads <= kSlots))) return cut_prompts(s, xb, sb, false);
     return c;
 }
 Cut cut_prompts(const la_shape_t *s, int xb, int sb) { return cut_prompts(s, xb, sb, xb == 2 && s->dv > 64); }

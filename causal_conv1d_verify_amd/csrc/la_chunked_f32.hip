@@ -268,7 +268,7 @@ ChunkedPlan plan() {
 }  // namespace
 
 ChunkedPlan pick_chunked_f32(int dk) {
-    ChunkedPlan p = dk <= 64 ? plan<4>() : dk <= 128 ? plan<8>() : dk <= 192 ? plan<12>() : plan<16>();
+    ChunkedPlan p = dk <= 64 ? plan<4>() : dk <= 96 ? plan<6>() : dk <= 128 ? plan<8>() : dk <= 192 ? plan<12>() : plan<16>();
     p.combine = pick_chunked(4, dk, false).combine;
     return p;
 }
