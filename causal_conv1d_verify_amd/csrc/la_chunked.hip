@@ -15,7 +15,20 @@
 // the state, the decayed products and (bf16 states) the decayed values, three for the decayed
 // values that build an fp32 state.  q.k of a chunk is shared: each wavefront makes its part of
 // the ten 16 x 16 tiles on and below the diagonal and leaves it in LDS in two parts.  k and v
-// are stored as they come and read transposed where a product needs their tokens in a lane.
+// are stored as they come and read transposed where a product needs their tokens in a lane; rows
+// in LDS are padded so that neither way of reading meets a bank twice.
+//
+// Measured: 8 prompts of 2048 tokens with 48 heads of 128 x 128 (fp32 state) 216 us; one of 16384
+// with 32 heads in 16 segments (bf16 state) 194 us, 60 of them the segments' own states and 14 their
+// sums.  What bounds it: the traffic (565 MB) would take 94 us, and the matrix instructions that the
+// parts make of it (a wavefront's 229 of 16 cycles a chunk) about 100; a chunk of two workgroups on a
+// compute unit takes 13,000 cycles, in which one wavefront's 600 vector instructions, at 4 to 5
+// cycles each, and its matrix instructions share the issue with the other's, and the clock goes from
+// 2.4 GHz with a few workgroups to 1.6-1.8 GHz with all of them.  Tried and slower: 8 wavefronts of
+// 16 columns (288 for 238 us at the time), tiles of 64 columns on a full chip (274 for 219), one
+// XCD's blocks contiguous.  Without effect: priorities, the compiler's order inside steps, loads and
+// stores past the caches.  Two parts instead of three for an fp32 state's values would save 9%, at
+// 2^-18 of each token's contribution for 2^-24.
 #include <type_traits>
 
 #include "la_matrix.h"
@@ -55,7 +68,7 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, g4 = 4 * (lane >> 4);
-    int rest = blockIdx.x;
+    int rest = shared_block(blockIdx.x, a.group * a.tiles, gridDim.x);
     const int tile = rest % a.tiles;
     rest /= a.tiles;
     const int h = rest % a.v_heads, id = rest / a.v_heads;

@@ -2,8 +2,9 @@
 // with fp32 products of 16 x 16 x 4, so no factor is taken apart.  A wavefront owns 16 of the
 // state's columns over all dk rows in registers, and its four rows of a register group are four
 // places of the product with q, read 16 bytes a lane.  v goes from memory to the lanes that use it.
-// Bound by the fp32 matrix rate (a sixteenth of bf16's): 32 of a chunk's 36 products a row tile are the
-// state's two.
+// Bound by the fp32 matrix rate (a sixteenth of bf16's), of which the state's two products take the
+// most, and at few rows by the length of a chain.  Measured: 5 prompts of up to 777 tokens, 6 heads of
+// 96 x 72, in segments of 128: 39 us (13 + 5 + 23 in its three kernels).
 #include "la_matrix.h"
 
 namespace laimpl {

@@ -100,6 +100,15 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// Workgroups go round the chip's 8 dies in turn, each with an L2 of its own.  Blocks in sets of
+// `set` that read the same q and k, in this order, lie on one die one after the other, and the sets
+// go round the dies (prompts: 1-3% faster, a third of q's and k's traffic with three v heads to one).
+__device__ __forceinline__ int shared_block(int b, int set, int blocks) {
+    const int round = 8 * set;
+    if (b >= blocks / round * round) return b;
+    return b / round * round + b % 8 * set + b / 8 % set;
+}
+
 // One row of a batch: its token count (-1: skip the row), its slot and its first elements.
 struct Row {
     int n;

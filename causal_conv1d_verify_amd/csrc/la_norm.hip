@@ -1,6 +1,10 @@
 // The gated RMS norm of each head, and the norm at a block's end.  Both hold a row in registers
 // between the sum of its squares and its scaling, so every element is read once and written
-// once, and both are bound by that traffic.
+// once, and both are bound by that traffic.  Measured: the gated norm of 16384 x 48 heads of 128 (bf16)
+// 116 us, 5.2 TB/s; the residual norm of 16384 x 4096 with an fp32 stream 163 us, 5.75 TB/s, of 1024 x
+// 5120 10.3 us.  Tried and no faster: two and four heads a lane group (118 and 132 us), stores past the
+// caches (no change), the weights asked for before the first sum (10.3 -> 11.8, 163 -> 169 us: fewer
+// wavefronts).
 #include "la_device.h"
 
 namespace laimpl {
