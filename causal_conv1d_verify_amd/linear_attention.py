@@ -2,7 +2,9 @@
 
 Thin Python binding of the C ABI in include/linear_attention.h (liblinattn.so), in the manner
 of the conv's: it marshals torch tensors, passes torch's current HIP stream, and computes
-nothing itself.
+nothing itself.  Calls on torch's current stream that are plainly in order are marshalled by the
+call module (csrc/la_call.cpp, 12 us less a call); the Python here takes all others, and says
+what is wrong with those that are refused.
 
     linear_attn_prefill(q, k, v, g, state, out, cu_seqlens, max_len=..., ...)
     linear_attn_update(q, k, v, g, state, out, ...)     T new tokens of each row, committed
