@@ -70,7 +70,7 @@ def _call_module():
     root = os.path.dirname(torch.__file__)
     return ([f"-I{sysconfig.get_paths()['include']}", f"-isystem{root}/include",
              f"-isystem{root}/include/torch/csrc/api/include", "-DUSE_ROCM",
-             "-D__HIP_PLATFORM_AMD__", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"],
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"],
             [f"-L{PKG}", "-llinattn", "-Wl,-rpath,$ORIGIN", f"-L{root}/lib", "-lc10", "-lc10_hip",
              "-ltorch_cpu", "-ltorch_python"])
 
