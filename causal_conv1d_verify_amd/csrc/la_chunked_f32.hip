@@ -4,7 +4,7 @@
 // places of the product with q, read 16 bytes a lane.  v goes from memory to the lanes that use it.
 // Bound by the fp32 matrix rate (a sixteenth of bf16's), of which the state's two products take the
 // most, and at few rows by the length of a chain.  Measured: 5 prompts of up to 777 tokens, 6 heads of
-// 96 x 72, in segments of 128: 39 us (13 + 5 + 23 in its three kernels).
+// 96 x 72, in segments of 128: 37 us (12 + 5 + 21 in its three kernels).
 #include "la_matrix.h"
 
 namespace laimpl {
@@ -30,7 +30,7 @@ struct Shared {
 
 // DT: row tiles of 16; OUT as in la_chunked.hip.
 template <int DT, bool OUT>
-__global__ __launch_bounds__(64 * W) void chunked_f32(const AttnArgs a) {
+__global__ __launch_bounds__(64 * W, 2) void chunked_f32(const AttnArgs a) {
     using SH = Shared<DT>;
     __shared__ SH sh;
     constexpr int COLS = 16 * W;
@@ -60,8 +60,11 @@ __global__ __launch_bounds__(64 * W) void chunked_f32(const AttnArgs a) {
         S[d] = f32x4{0, 0, 0, 0};
         if (!OUT || !init) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (in_cols && 16 * d + g4 + i < a.dk) S[d][i] = state[(16 * d + g4 + i) * a.dv];
+        for (int i = 0; i < 4; ++i) {              // loads without branches, as in la_chunked.hip
+            const bool in = in_cols && 16 * d + g4 + i < a.dk;
+            const float x = in_cols ? state[in ? (16 * d + g4 + i) * a.dv : 0] : 0.0f;
+            S[d][i] = in ? x : 0.0f;
+        }
     }
     const int64_t ws_head = ((int64_t)id * a.v_heads + h) * a.tiles + tile;
     const int64_t ws_step = (int64_t)a.v_heads * a.tiles;
@@ -87,9 +90,16 @@ __global__ __launch_bounds__(64 * W) void chunked_f32(const AttnArgs a) {
     constexpr int B = DT / 2;
     const int r0 = tid >> 3, f0 = 4 * (tid & 7);
     f32x4 rq[OUT ? B : 1], rk[B];
-    float v[8];                                    // tokens 16 x + g4 + i of the lane's column
+    float rv[8];                                   // tokens 16 x + g4 + i of the lane's column
     auto fetch = [&](int left) {
         const uint32_t t = r0 < left ? r0 : left - 1;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int at = 16 * (x / 4) + g4 + x % 4;
+            const uint32_t tv = at < left ? at : left - 1;
+            rv[x] = *reinterpret_cast<const float *>(gv + (tv * v_step + (in_cols ? 4 * col : 0)));
+        }
+        gv += (int64_t)C * v_step;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             const uint32_t c = f0 + 32 * b < a.dk ? 4 * (f0 + 32 * b) : 0;
@@ -136,14 +146,9 @@ __global__ __launch_bounds__(64 * W) void chunked_f32(const AttnArgs a) {
 
     for (int t0 = 0, turn = 0; t0 < n; t0 += C, turn ^= 1) {
         stage(n - t0);
+        float v[8];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * x + g4 + i;
-                v[4 * x + i] = in_cols && t0 + t < n ? *reinterpret_cast<const float *>(gv + (t * v_step + 4 * col)) : 0.0f;
-            }
-        gv += (int64_t)C * v_step;
+        for (int x = 0; x < 8; ++x) v[x] = in_cols && t0 + 16 * (x / 4) + g4 + x % 4 < n ? rv[x] : 0.0f;
         __syncthreads();
         const Decays32 &dec = sh.d[turn];
         const float keep = dec.total;

@@ -154,7 +154,7 @@ __device__ __forceinline__ void store_one(Bf16 *p, float x) {
 struct Segment { int row, index; bool last; };
 __device__ __forceinline__ int segments_of(const AttnArgs &a, int i) {
     const Row r = row_of(a, i);
-    return r.n < 0 ? 0 : r.n == 0 ? 1 : (int)(((int64_t)r.n + a.seg_len - 1) / a.seg_len);
+    return r.n < 0 ? 0 : r.n == 0 ? 1 : (int)(((uint32_t)r.n + (uint32_t)a.seg_len - 1) / (uint32_t)a.seg_len);
 }
 template <int W>
 __device__ __forceinline__ Segment find_segment(const AttnArgs &a, int id, int64_t *shared) {
