@@ -13,7 +13,7 @@
 // of the rows meet once, in LDS.  bf16 parts of 32-bit factors are as for prompts.
 //
 // Measured: one token for 256 rows x 32 heads of 128 x 128 (fp32 state, a tenth of the rows padded)
-// 165 us, 6.0 TB/s; eight for 128 rows x 48 heads, verify and commit, 178 us, 6.5 TB/s.  States
+// 166 us, 6.0 TB/s; eight for 128 rows x 48 heads, verify and commit, 185 us, 6.2 TB/s.  States
 // past the Infinity Cache's reach go past it (184 and 209 us through it).
 #include <type_traits>
 
@@ -63,25 +63,27 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
                     each(b, e, u, r, in_cols && r < a.dk);
                 }
     };
-    ST *state = static_cast<ST *>(a.state) + row.slot * a.s_slot + (int64_t)h * a.dk * a.dv + c0;
+    ST *state = static_cast<ST *>(a.state) + row.slot * a.s_slot + (int64_t)h * a.dk * a.dv;
     auto load = [&](auto stream) {
         rows_of_state([&](int b, int e, int u, int r, bool in) {
             float f[4] = {};
-            if (in) load_vec<4, decltype(stream)::value>(state + r * a.dv, f);
+            if (decltype(stream)::value ? in : true) load_vec<4, decltype(stream)::value>(state + (in ? r * a.dv + c0 : 0), f);
 #pragma unroll
-            for (int nc = 0; nc < NC; ++nc) S[b][e][nc][u] = f[nc];
+            for (int nc = 0; nc < NC; ++nc) S[b][e][nc][u] = in ? f[nc] : 0.0f;
         });
     };
+    // Where states are streamed they are the call's work and go first; where they are few the tokens'
+    // own products are made while the state is on its way (8 rows x 17 tokens, 32 heads, verify and
+    // commit: 12.5 us for 17.8).
     if (a.streaming) load(std::true_type{});
-    else load(std::false_type{});
 
-    // ---- the tokens, at the places 4g + u and 16 + 4g + u of a sum over 32
-    const Bf16 *gq = OUT ? static_cast<const Bf16 *>(a.q) + row.q + hq * a.q_head + r0 + g4 : nullptr;
+    // ---- the tokens, at the places 4g + u and 16 + 4g + u of a sum over 32.  What is not there is read
+    // from the first place that is, without a branch, and zeroed.
     const Bf16 *gk = static_cast<const Bf16 *>(a.k) + row.k + hq * a.k_head;
-    const Bf16 *gv = static_cast<const Bf16 *>(a.v) + row.v + h * a.v_head + c0;
     const u32x2 none = {0, 0};
     bf16x8 qf[OUT ? TT : 1][RB], kf[OUT ? TT : 1][RB];
-    if constexpr (OUT)
+    if constexpr (OUT) {
+        const Bf16 *gq = static_cast<const Bf16 *>(a.q) + row.q + hq * a.q_head;
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -89,28 +91,48 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
                 u32x2 q[2], k[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int at = 32 * b + 16 * e;
-                    const bool in = 16 * t + j < n && r0 + at + g4 < a.dk;
-                    q[e] = in ? *reinterpret_cast<const u32x2 *>(gq + (16 * t + j) * a.q_tok + at) : none;
-                    k[e] = in ? *reinterpret_cast<const u32x2 *>(gk + (16 * t + j) * a.k_tok + r0 + g4 + at) : none;
+                    const int at = r0 + g4 + 32 * b + 16 * e;
+                    const bool in = 16 * t + j < n && at < a.dk;
+                    q[e] = *reinterpret_cast<const u32x2 *>(gq + (in ? (16 * t + j) * a.q_tok + at : 0));
+                    k[e] = *reinterpret_cast<const u32x2 *>(gk + (in ? (16 * t + j) * a.k_tok + at : 0));
+                    q[e] = in ? q[e] : none;
+                    k[e] = in ? k[e] : none;
                 }
                 qf[t][b] = frag(q[0], q[1]);
                 kf[t][b] = frag(k[0], k[1]);
             }
+    }
+    const Bf16 *gv = static_cast<const Bf16 *>(a.v) + row.v + h * a.v_head;
     u32x2 v[2][4];                                 // tokens 16 t + g4 + u, columns c0 to c0 + 3
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            v[t][u] = t < TT && in_cols && 16 * t + g4 + u < n
-                          ? *reinterpret_cast<const u32x2 *>(gv + (16 * t + g4 + u) * a.v_tok) : none;
+        for (int u = 0; u < 4; ++u) {
+            v[t][u] = none;
+            if (t >= TT) continue;
+            const bool in = in_cols && 16 * t + g4 + u < n;
+            v[t][u] = *reinterpret_cast<const u32x2 *>(gv + (in ? (16 * t + g4 + u) * a.v_tok + c0 : 0));
+            v[t][u] = in ? v[t][u] : none;
+        }
     const float g = a.g && lane < n ? a.g[row.g + h + lane * a.g_tok] : 0.0f;
+    constexpr int PIECES = WRITE ? (16 * TT * 8 * RB + 255) / 256 : 0;   // of k for LDS, of a thread
+    u32x4 rk[WRITE ? PIECES : 1];
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+        const int at = tid + 256 * p, t = at / (8 * RB), c = 8 * (at % (8 * RB));
+        const bool in = t < n && c < a.dk;
+        const u32x4 zero = {0, 0, 0, 0};
+        rk[p] = *reinterpret_cast<const u32x4 *>(gk + (in ? t * a.k_tok + c : 0));
+        rk[p] = in ? rk[p] : zero;
+    }
+
+    if (!a.streaming) load(std::false_type{});
+
     if constexpr (WRITE) {
-        for (int at = tid; at < 16 * TT * 8 * RB; at += 256) {
-            const int t = at / (8 * RB), c = 8 * (at % (8 * RB));
-            const u32x4 zero = {0, 0, 0, 0};
-            *reinterpret_cast<u32x4 *>(sk + t * KP + 2 * c) =
-                t < n && c < a.dk ? *reinterpret_cast<const u32x4 *>(gk + t * a.k_tok + c) : zero;
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) {
+            const int at = tid + 256 * p, t = at / (8 * RB), c = 8 * (at % (8 * RB));
+            if (at < 16 * TT * 8 * RB) *reinterpret_cast<u32x4 *>(sk + t * KP + 2 * c) = rk[p];
         }
         __syncthreads();
     }
@@ -140,25 +162,6 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
 
     f32x4 o[OUT ? TT : 1][NC];
     if constexpr (OUT) {
-        // ---- S^T q, transposed: lane = token
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int nc = 0; nc < NC; ++nc) o[t][nc] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int nc = 0; nc < NC; ++nc) {
-                float f[8];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) f[u] = S[b][0][nc][u], f[4 + u] = S[b][1][nc][u];
-#pragma unroll
-                for (int part = 0; part < SPARTS; ++part) {
-                    const bf16x8 s = take_part(f);
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) o[t][nc] = mma(s, qf[t][b], o[t][nc]);
-                }
-            }
         // ---- the tokens' own products.  Values that are not finite are taken out: a masked product
         // of 0 must not carry them to the tokens before theirs; what they reach is marked.
         bf16x8 clean[NC], bad[NC];
@@ -173,11 +176,9 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
         const bool any_bad = __any(some != 0);
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const float thi = dec.hi[wave][16 * t + j], tlo = dec.lo[wave][16 * t + j], in = dec.in[wave][16 * t + j];
+            const float thi = dec.hi[wave][16 * t + j], tlo = dec.lo[wave][16 * t + j];
 #pragma unroll
-            for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) o[t][nc][u] *= in;
+            for (int nc = 0; nc < NC; ++nc) o[t][nc] = f32x4{0, 0, 0, 0};
             float f[8] = {};
             u32x4 below = {0, 0, 0, 0};            // 1 where token s <= t
 #pragma unroll
@@ -212,6 +213,34 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
                     for (int u = 0; u < 4; ++u)
                         if (reached[u] > 0.0f) o[t][nc][u] = NAN;
                 }
+        }
+        // ---- S^T q, transposed: lane = token
+        f32x4 old[TT][NC];
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc) old[t][nc] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc) {
+                float f[8];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) f[u] = S[b][0][nc][u], f[4 + u] = S[b][1][nc][u];
+#pragma unroll
+                for (int part = 0; part < SPARTS; ++part) {
+                    const bf16x8 s = take_part(f);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) old[t][nc] = mma(s, qf[t][b], old[t][nc]);
+                }
+            }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const float in = dec.in[wave][16 * t + j];
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) o[t][nc][u] = fmaf(old[t][nc][u], in, o[t][nc][u]);
         }
         if (wave >= 2)
 #pragma unroll
@@ -277,7 +306,7 @@ __global__ __launch_bounds__(256) void few(const AttnArgs a) {
         auto store = [&](auto stream) {
             rows_of_state([&](int b, int e, int u, int r, bool in) {
                 const float f[4] = {S[b][e][0][u], S[b][e][1][u], S[b][e][2][u], S[b][e][3][u]};
-                if (in) store_vec<4, decltype(stream)::value>(state + r * a.dv, f);
+                if (in) store_vec<4, decltype(stream)::value>(state + (r * a.dv + c0), f);
             });
         };
         if (a.streaming) store(std::true_type{});
