@@ -178,13 +178,13 @@ int recurrent(laimpl::AttnArgs a, int xb, int sb, void *stream) {
 // Along a row: its tokens are one chain of chunks in one workgroup unless that chain is much
 // longer than the share of all chunks that each of the chip's slots would have (two workgroups on
 // each of 256 compute units): then rows are cut into segments of about that share, at the price
-// of passing over their k and v twice (one prompt of 16384 with 32 heads: 202 us in 16
+// of passing over their k and v twice (one prompt of 16384 with 32 heads: 192 us in 16
 // segments).
 //
-// Across a head (bf16 tokens; fp32 ones go in tiles of 64): tiles of 128 columns, since what a chunk reads and the products q.k serve all of
-// a tile; tiles of 64 where the wide ones would leave most compute units empty (64 workgroups of
+// Across a head (bf16 tokens; fp32 ones go in tiles of 64): tiles of 128 columns, since what a
+// chunk reads and the products q.k serve all of a tile; tiles of 64 where the wide ones would leave most compute units empty (64 workgroups of
 // 32 chunks: 122 us for 160) or the state's way in and out counts, in a few chunks of one
-// generation of workgroups (8 rows of up to 160 tokens, 48 heads: 25 us for 27).
+// generation of workgroups (8 rows of up to 160 tokens, 48 heads: 21 us for 27).
 struct Cut {
     laimpl::ChunkedPlan plan;
     int64_t tiles, segments, ws_states, ws_bytes;
