@@ -1,4 +1,4 @@
-// Packed prompts of fp32 tokens, in chunks of 32: the formulas and the division of la_chunked.hip
+// Packed prompts of fp32 tokens (and 12 to 32 tokens of each row, as one chunk), in chunks of 32: the formulas and the division of la_chunked.hip
 // with fp32 products of 16 x 16 x 4, so no factor is taken apart.  A wavefront owns 16 of the
 // state's columns over all dk rows in registers, and its four rows of a register group are four
 // places of the product with q, read 16 bytes a lane.  v goes from memory to the lanes that use it.
@@ -82,11 +82,12 @@ __global__ __launch_bounds__(64 * W, 2) void chunked_f32(const AttnArgs a) {
     }
 
     // ---- a chunk's q and k: 8 threads a row, 32 floats apart by block
-    const char *gq = OUT ? reinterpret_cast<const char *>(static_cast<const float *>(a.q) + row.q + hq * a.q_head + first * a.q_tok)
-                         : nullptr;
     const char *gk = reinterpret_cast<const char *>(static_cast<const float *>(a.k) + row.k + hq * a.k_head + first * a.k_tok);
     const char *gv = reinterpret_cast<const char *>(static_cast<const float *>(a.v) + row.v + h * a.v_head + first * a.v_tok);
-    const uint32_t q_step = 4 * (uint32_t)a.q_tok, k_step = 4 * (uint32_t)a.k_tok, v_step = 4 * (uint32_t)a.v_tok;
+    // (a commit has no q and no outputs: k stands in, and nothing of what it makes is stored)
+    const char *gq = OUT && a.q ? reinterpret_cast<const char *>(static_cast<const float *>(a.q) + row.q + hq * a.q_head + first * a.q_tok)
+                                : gk;
+    const uint32_t k_step = 4 * (uint32_t)a.k_tok, v_step = 4 * (uint32_t)a.v_tok, q_step = a.q ? 4 * (uint32_t)a.q_tok : k_step;
     constexpr int B = DT / 2;
     const int r0 = tid >> 3, f0 = 4 * (tid & 7);
     f32x4 rq[OUT ? B : 1], rk[B];
@@ -243,7 +244,7 @@ __global__ __launch_bounds__(64 * W, 2) void chunked_f32(const AttnArgs a) {
                         if (reached[i] > 0.0f) o[r][i] = NAN;
                 }
                 const int t = 16 * r + j, c = tile * COLS + 16 * wave + g4;
-                if (t0 + t < n && c < a.dv) *reinterpret_cast<f32x4 *>(out + (t * o_step + 4 * c)) = o[r];
+                if (a.out && t0 + t < n && c < a.dv) *reinterpret_cast<f32x4 *>(out + (t * o_step + 4 * c)) = o[r];
             }
             out += (int64_t)C * o_step;
         }
@@ -251,7 +252,7 @@ __global__ __launch_bounds__(64 * W, 2) void chunked_f32(const AttnArgs a) {
     }
 
     if constexpr (OUT) {
-        if (!seg.last) return;
+        if (!seg.last || !a.write_state) return;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll

@@ -9,7 +9,7 @@
 // out sums over the rows: in the lane, across the wavefront's groups, and across the four
 // wavefronts through LDS (always in the same order).
 //
-// It takes fp32 tokens one after the other (up to 32 of them), the single tokens of few rows, where
+// It takes few fp32 tokens one after the other, the single tokens of few rows, where
 // it starts sooner than the matrix form (one row of 48 heads, 128 x 128, fp32 state: 4.4 us a call,
 // 5.0 of the kernel traced alone, for 6.5 us), and prompts whose tokens lie too far apart for 32-bit
 // offsets.  For one token it is bound by the state, read and written once.

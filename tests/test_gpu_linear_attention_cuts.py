@@ -177,3 +177,58 @@ def test_streamed_states_are_the_same(T, name):
         results.append((S, out))
     assert all(torch.equal(a, b) for a, b in zip(*results))
     assert torch.equal(results[0][0], pool) == (name == "linear_attn_verify")
+
+
+@pytest.mark.parametrize("shape", [(5, 1, 2, 200, 72), (3, 2, 2, 64, 256)], ids=str)
+@pytest.mark.parametrize("T", [11, 12, 15, 16, 20, 32])
+def test_commit_counts_and_rejected_tokens_of_a_chunk(T, shape):
+    """fp32 tokens on both sides of where they go as one chunk: counts of none, some, all and out
+    of range, and rejected tokens that are not finite."""
+    n, hq, hv, dk, dv = shape
+    _say("commit chunk", T, shape)
+    import causal_conv1d_verify_amd as cv
+
+    p = Problem([T] * n, hq, hv, dk, dv, "f32", packed=False, T=T, pads=(1,))
+    counts = [T, 3, 0, T + 1, -1][:n]
+    live = [i for i in range(n) if 0 <= counts[i] <= T and i != 1]
+    want = p.expected(counts=[c if i in live else 0 for i, c in enumerate(counts)])
+    for i, c in enumerate(counts):
+        if 0 <= c < T:
+            p.k[i, c:] = math.nan
+            p.v[i, c:] = math.inf
+            p.g[i, c:] = math.nan
+    num = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    cv.linear_attn_commit(p.k, p.v, p.g, p.pool, num, slot_idx=p.slot_idx)
+    torch.cuda.synchronize()
+    p.check(want, outputs=False, live=live)
+    for i in live:
+        if counts[i] == 0:
+            assert torch.equal(p.pool_full[p.slots[i].long()].cpu(), p.before[p.slots[i].long()])
+
+
+@pytest.mark.parametrize("name", ["linear_attn_update", "linear_attn_verify"])
+@pytest.mark.parametrize("T", [12, 23, 32])
+def test_a_chunk_of_few_tokens_with_strong_decays_and_not_finite(T, name):
+    _say("chunk extreme", T, name)
+    import causal_conv1d_verify_amd as cv
+
+    p = Problem([T] * 3, 1, 2, 64, 72, "f32", packed=False, T=T, pads=(2,))
+    g = p.g.cpu()
+    g[0, 4] = -math.inf
+    g[1, 2] = -500.0
+    p.g = g.cuda()
+    want = p.expected()
+    p.v[1, 9] = math.nan
+    getattr(cv, name)(p.q, p.k, p.v, p.g, p.pool, p.out, slot_idx=p.slot_idx)
+    torch.cuda.synchronize()
+    got = p.out.cpu()
+    for i, upto in ((0, T), (1, 9)):
+        a = ref.bounds(want[0][i, :upto], want[2][i, :upto], p.xt, p.xt, p.dk, p.T)
+        ref.check(got[i, :upto], want[0][i, :upto], a, f"row {i}")
+    assert not torch.isfinite(got[1, 9:]).any()
+    slots = [int(s) for s in p.slots]
+    if name == "linear_attn_verify":
+        assert torch.equal(p.pool_full.cpu(), p.before)
+    else:
+        a = ref.bounds(want[1][0], want[3][0], p.st, p.xt, p.dk, p.T)
+        ref.check(p.pool[slots[0]].cpu(), want[1][0], a, "state")
