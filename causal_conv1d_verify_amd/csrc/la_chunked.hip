@@ -26,7 +26,7 @@
 // compute unit takes 13,000 cycles, in which one wavefront's 600 vector instructions, at 4 to 5
 // cycles each, and its matrix instructions share the issue with the other's, and the clock goes from
 // 2.4 GHz with a few workgroups to 1.6-1.8 GHz with all of them.  Tried and slower: 8 wavefronts of
-// 16 columns (288 for 238 us at the time), tiles of 64 columns on a full chip (274 for 219), one
+// 16 columns (288 for 238 us at the time), tiles of 64 columns on a full chip (231 for 213), one
 // XCD's blocks contiguous.  Without effect: priorities, the compiler's order inside steps, loads and
 // stores past the caches.  Two parts instead of three for an fp32 state's values would save 9%, at
 // 2^-18 of each token's contribution for 2^-24.
