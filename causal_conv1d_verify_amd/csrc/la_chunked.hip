@@ -58,7 +58,8 @@ struct Shared {
 };
 
 // KT: dk in blocks of 32; W: wavefronts; NC: column tiles of 16 of each; OUT: outputs are wanted, else
-// only what a segment's tokens leave in a state that starts from zeros.
+// only what a segment's tokens leave in a state that starts from zeros, and, in the place of a row's
+// last segment, the state that the row starts from.
 template <int KT, int NC, typename ST, bool OUT>
 __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(const AttnArgs a) {
     constexpr int PARTS = sizeof(ST) == 4 ? 3 : 2;
@@ -72,14 +73,14 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
     int rest = shared_block(blockIdx.x, a.group * a.tiles, gridDim.x);
     const int tile = rest % a.tiles;
     rest /= a.tiles;
-    const int h = rest % a.v_heads, id = rest / a.v_heads;
+    const int h = uniform(rest % a.v_heads), id = uniform(rest / a.v_heads);
     const int hq = h / a.group;
 
     const Segment seg = find_segment<W>(a, id, sh.found);
     if (seg.row < 0) return;                       // same for the workgroup
     const Row row = uniform(row_of(a, seg.row));
     const bool init = !a.has_init || uniform(a.has_init[seg.row]) != 0;
-    if (!OUT && seg.last) return;
+    if (!OUT && seg.last && seg.index == 0) return;
     if (OUT && row.n == 0 && init) return;
     const int first = seg.index * a.seg_len;
     const int n = (row.n - first < a.seg_len ? row.n - first : a.seg_len);
@@ -90,41 +91,53 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
     // outputs of a lane are 4 * NC columns side by side
     auto column = [&](int nc, int x) { return NC == 2 ? colw + 8 * (x / 4) + 4 * nc + x % 4 : colw + x; };
 
-    // ---- the state that enters the segment
-    f32x4 S[NC][DT];
+    // ---- the state that enters the segment.  Of a row in one segment it is in the pool.  Where a row
+    // is cut its last segment writes the pool at a time that the others know nothing of, so the pool is
+    // read before that, by the launch without outputs (the last segment's workgroup, which has nothing
+    // else to do there), and every segment takes its state from the workspace.
     ST *state = static_cast<ST *>(a.state) + row.slot * a.s_slot + (int64_t)h * a.dk * a.dv;
+    auto from_pool = [&](int nc, int d) {          // loads without branches, the first place where there is none
+        f32x4 f;
+        const int c = col0 + column(nc, j);
 #pragma unroll
-    for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            S[nc][d] = f32x4{0, 0, 0, 0};
-            if (!OUT || !init) continue;
-            const int c = col0 + column(nc, j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {          // loads without branches, the first place where there is none
-                const int r = 16 * d + g4 + i;
-                const bool in = r < a.dk && c < a.dv;
-                const float x = load_one(state + (in ? r * a.dv + c : 0));
-                S[nc][d][i] = in ? x : 0.0f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int r = 16 * d + g4 + i;
+            const bool in = r < a.dk && c < a.dv;
+            const float x = load_one(state + (in ? r * a.dv + c : 0));
+            f[i] = in ? x : 0.0f;
         }
+        return f;
+    };
     const int64_t ws_head = ((int64_t)id * a.v_heads + h) * a.tiles + tile;
     const int64_t ws_step = (int64_t)a.v_heads * a.tiles;          // from segment to segment
     constexpr int64_t WS = (int64_t)64 * W * NC * DT;              // f32x4 of one workgroup
+    f32x4 S[NC][DT];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) S[nc][d] = f32x4{0, 0, 0, 0};
     if constexpr (OUT) {
-        if (seg.index > 0) {                       // what the segments before leave, and their decay
-            float keep = 1.0f;
-            for (int s = seg.index; s > 0; --s) keep *= a.ws_total[ws_head - s * ws_step];
-            const f32x4 *w = static_cast<const f32x4 *>(a.ws) + (ws_head - ws_step) * WS + tid;
+        const bool cut = seg.index > 0 || !seg.last;
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                if (init && !cut) S[nc][d] = from_pool(nc, d);
+        if (cut) {                                 // the one before has it; the first one's is in the last one's place
+            const int64_t at = seg.index > 0 ? ws_head - ws_step : ws_head + (row.n - 1) / a.seg_len * ws_step;
+            const f32x4 *w = static_cast<const f32x4 *>(a.ws) + at * WS + tid;
 #pragma unroll
             for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const f32x4 x = w[(nc * DT + d) * 64 * W];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[nc][d][i] = fmaf(S[nc][d][i], keep, x[i]);
-                }
+                for (int d = 0; d < DT; ++d) S[nc][d] = w[(nc * DT + d) * 64 * W];
         }
+    } else if (seg.last) {
+        f32x4 *w = static_cast<f32x4 *>(a.ws) + ws_head * WS + tid;
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) w[(nc * DT + d) * 64 * W] = init ? from_pool(nc, d) : S[nc][d];
+        return;
     }
 
     // ---- staging of a chunk: global memory -> registers -> LDS.  Eight lanes take 128 bytes of a
@@ -522,9 +535,10 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
     }
 }
 
-// Between the two: each segment's place in the workspace, which holds what its own tokens leave, is
-// left with what all of the row's up to it leave.  A workgroup has 256 vectors of one (row, v head,
-// tile), far apart from segment to segment; eight segments' are in flight at once.
+// Between the two: each segment's place in the workspace, which holds what its own tokens leave in a
+// state of zeros, is left with the state behind it, from the row's first state in the last one's place.
+// A workgroup has 256 vectors of one (row, v head, tile), far apart from segment to segment; eight
+// segments' are in flight at once.
 __global__ __launch_bounds__(64 * W) void combine(const AttnArgs a, const int vectors) {
     const int parts = vectors / (64 * W);
     int rest = blockIdx.x;
@@ -538,7 +552,7 @@ __global__ __launch_bounds__(64 * W) void combine(const AttnArgs a, const int ve
     const int64_t step = (int64_t)a.v_heads * a.tiles, at = id * step + ht;
     f32x4 *w = static_cast<f32x4 *>(a.ws) + at * vectors + part * (64 * W) + threadIdx.x;
     const float *total = a.ws_total + at;
-    f32x4 S = {0, 0, 0, 0};
+    f32x4 S = w[(count - 1) * step * vectors];
     constexpr int AHEAD = 8;
     for (int s0 = 0; s0 < count - 1; s0 += AHEAD) {
         f32x4 x[AHEAD];

@@ -39,46 +39,53 @@ __global__ __launch_bounds__(64 * W, 2) void chunked_f32(const AttnArgs a) {
     int rest = blockIdx.x;
     const int tile = rest % a.tiles;
     rest /= a.tiles;
-    const int h = rest % a.v_heads, id = rest / a.v_heads;
+    const int h = uniform(rest % a.v_heads), id = uniform(rest / a.v_heads);
     const int hq = h / a.group;
     const Segment seg = find_segment<W>(a, id, sh.found);
     if (seg.row < 0) return;                       // same for the workgroup
     const Row row = uniform(row_of(a, seg.row));
     const bool init = !a.has_init || uniform(a.has_init[seg.row]) != 0;
-    if (!OUT && seg.last) return;
+    if (!OUT && seg.last && seg.index == 0) return;
     if (OUT && row.n == 0 && init) return;
     const int first = seg.index * a.seg_len;
     const int n = row.n - first < a.seg_len ? row.n - first : a.seg_len;
 
-    // ---- the state that enters the segment
+    // ---- the state that enters the segment, as in la_chunked.hip
     const int col = tile * COLS + 16 * wave + j;
     const bool in_cols = col < a.dv;
     float *state = static_cast<float *>(a.state) + row.slot * a.s_slot + (int64_t)h * a.dk * a.dv + col;
-    f32x4 S[DT];
+    auto from_pool = [&](int d) {
+        f32x4 f;
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-        S[d] = f32x4{0, 0, 0, 0};
-        if (!OUT || !init) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {              // loads without branches, as in la_chunked.hip
+        for (int i = 0; i < 4; ++i) {
             const bool in = in_cols && 16 * d + g4 + i < a.dk;
             const float x = in_cols ? state[in ? (16 * d + g4 + i) * a.dv : 0] : 0.0f;
-            S[d][i] = in ? x : 0.0f;
+            f[i] = in ? x : 0.0f;
         }
-    }
+        return f;
+    };
     const int64_t ws_head = ((int64_t)id * a.v_heads + h) * a.tiles + tile;
     const int64_t ws_step = (int64_t)a.v_heads * a.tiles;
     constexpr int64_t WS = (int64_t)64 * W * DT;
-    if (OUT && seg.index > 0) {
-        float keep = 1.0f;
-        for (int s = seg.index; s > 0; --s) keep *= a.ws_total[ws_head - s * ws_step];
-        const f32x4 *w = static_cast<const f32x4 *>(a.ws) + (ws_head - ws_step) * WS + tid;
+    f32x4 S[DT];
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            const f32x4 x = w[d * 64 * W];
+    for (int d = 0; d < DT; ++d) S[d] = f32x4{0, 0, 0, 0};
+    if constexpr (OUT) {
+        const bool cut = seg.index > 0 || !seg.last;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[d][i] = fmaf(S[d][i], keep, x[i]);
+        for (int d = 0; d < DT; ++d)
+            if (init && !cut) S[d] = from_pool(d);
+        if (cut) {
+            const int64_t at = seg.index > 0 ? ws_head - ws_step : ws_head + (row.n - 1) / a.seg_len * ws_step;
+            const f32x4 *w = static_cast<const f32x4 *>(a.ws) + at * WS + tid;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) S[d] = w[d * 64 * W];
         }
+    } else if (seg.last) {
+        f32x4 *w = static_cast<f32x4 *>(a.ws) + ws_head * WS + tid;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) w[d * 64 * W] = init ? from_pool(d) : S[d];
+        return;
     }
 
     // ---- a chunk's q and k: 8 threads a row, 32 floats apart by block

@@ -32,8 +32,9 @@ struct AttnArgs {
     // prompts in chunks: a row is cut into segments of seg_len tokens (a multiple of the chunk;
     // rows of at most seg_len tokens are one)
     int32_t seg_len, segments;          // segments that the grid and the workspace hold
-    void *ws;                           // what each segment but a row's last adds to a state
-    float *ws_total;                    // and the decay over it
+    void *ws;                           // what each segment adds to a state (a row's last: the row's
+                                        // first state), then the state behind it
+    float *ws_total;                    // the decay over each
 };
 
 struct NormArgs {
@@ -55,7 +56,8 @@ struct RecurrentPlan {
 RecurrentPlan pick_recurrent(int x_bytes, int state_bytes, int dk, bool wide);
 
 // Prompts in chunks.  Where rows are cut, `first` leaves what each segment's tokens add to a state
-// in the workspace and `combine` adds up those of a row; `run` makes the outputs and the last state.
+// and the row's first state in the workspace, `combine` makes the state behind each segment of them;
+// `run` makes the outputs and the last state, and of a cut row it does not read the pool that it writes.
 struct ChunkedPlan {
     const void *run, *first, *combine;
     int cols, threads, chunk;     // columns of the state per workgroup; tokens of a chunk
