@@ -169,9 +169,14 @@ def _attn_args(kind, q, k, v, g, state, out, *, cu_seqlens=None, max_len=None, s
         if need < 0:
             raise LinAttnError(need, _linattn.error_message(lib, need))
         if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            if handle != torch.cuda.current_stream(dev).cuda_stream:
-                workspace.record_stream(torch.cuda.ExternalStream(handle, device=dev))
+            # a block of the stream that the call runs on: one that another stream gave up may
+            # still be in use by what is queued there
+            if handle == torch.cuda.current_stream(dev).cuda_stream:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:
+                with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev) if handle
+                                       else torch.cuda.default_stream(dev)):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
         fn, args = lib.linattn_prefill, (ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state),
                                          _ptr(slot_idx), _ptr(cu_seqlens), _ptr(has_initial_state),
