@@ -144,6 +144,11 @@ def _attn_args(kind, q, k, v, g, state, out, *, cu_seqlens=None, max_len=None, s
         _int32_vec("cu_seqlens", cu_seqlens, n_seq + 1)
         _int32_vec("has_initial_state", has_initial_state, n_seq)
         dims = (0, 1)
+        if v.shape[0] == 0:
+            # no tokens at all, though states may start from zeros: the token tensors hold no
+            # element to point at, and one token that is neither read nor written stands in
+            T = 1
+            q, k, v, out = (t.new_empty(1, *t.shape[1:]) for t in (q, k, v, out))
     else:
         n_seq, T = v.shape[0], v.shape[1]
         _int32_vec("num_tokens", num_tokens, n_seq)
@@ -160,10 +165,6 @@ def _attn_args(kind, q, k, v, g, state, out, *, cu_seqlens=None, max_len=None, s
         v.shape[0] if packed else 0)
     handle = _on_stream(stream, dev)
     ref = ctypes.byref(shape)
-    if packed and n_seq and v.shape[0] == 0:
-        # no tokens at all, though states may start from zeros: the token tensors hold no
-        # element to point at, and none is read or written
-        q = k = v = out = state
     if packed:
         need = lib.linattn_prefill_workspace(ref)
         if need < 0:
