@@ -103,7 +103,10 @@ int check_attn(const la_shape_t *s, const Need &need, int *xb, int *sb, bool *em
                     (long long)s->state_slot_stride, (long long)per_slot);
     if (need.packed && s->tokens < 0) return fail(CV_EINVAL, "tokens (%lld) is negative", (long long)s->tokens);
     if (need.out) {
-        Dim d[3] = {{s->v_heads, s->out_head_stride}, {s->T, s->out_tok_stride},
+        // of packed rows the tokens of all together; where they are not known, what would overlap
+        // with any two of them (T bounds a row, and says nothing of their number)
+        const int64_t toks = !need.packed ? s->T : s->tokens > 0 ? s->tokens : std::min<int64_t>(2, sat_mul(s->n_seq, s->T));
+        Dim d[3] = {{s->v_heads, s->out_head_stride}, {toks, s->out_tok_stride},
                     {need.packed ? 1 : s->n_seq, s->out_seq_stride}};
         if (!apart(s->dv, d, 3)) return fail(CV_EINVAL, "the strides of out make its rows overlap");
     }

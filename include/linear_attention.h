@@ -76,7 +76,8 @@ typedef struct la_shape {
     int64_t g_seq_stride, g_tok_stride;
     int64_t state_slot_stride;   /* >= v_heads*dk*dv if n_slots > 1                         */
     int64_t tokens;       /* prefill: tokens of all rows together, or 0 if that is not known;
-                             sizes the grid and the workspace                               */
+                             sizes the grid and the workspace, and tells whether the strides
+                             of out keep its elements apart (not known: of any two tokens)  */
 } la_shape_t;
 
 /*
