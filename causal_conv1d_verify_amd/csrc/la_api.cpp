@@ -205,7 +205,8 @@ Cut cut_prompts(const la_shape_t *s, int xb, int sb, bool wide) {
     const int64_t heads = s->v_heads * c.tiles;
     int64_t tokens = sat_mul(s->n_seq, s->T);
     if (s->tokens > 0 && s->tokens < tokens) tokens = s->tokens;
-    const int64_t chain = (s->T + chunk - 1) / chunk;
+    // (no row holds more than all tokens together, however far T bounds it)
+    const int64_t chain = (std::min<int64_t>(s->T, tokens) + chunk - 1) / chunk;
     const int64_t share = std::max(kLeast, sat_mul(tokens / chunk + 1, heads) / kSlots);
     const int64_t segments = tokens / (share * chunk) + s->n_seq;
     const int64_t states = sat_mul(segments, heads);
