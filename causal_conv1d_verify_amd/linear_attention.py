@@ -141,6 +141,8 @@ def _attn_args(kind, q, k, v, g, state, out, *, cu_seqlens=None, max_len=None, s
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise ValueError("cu_seqlens must hold n_seq + 1 offsets")
         n_seq, T = cu_seqlens.shape[0] - 1, max(1, int(max_len))
+        if T > 2 ** 31 - 1:
+            raise ValueError(f"max_len ({T}) is over 2^31 - 1")
         _int32_vec("cu_seqlens", cu_seqlens, n_seq + 1)
         _int32_vec("has_initial_state", has_initial_state, n_seq)
         dims = (0, 1)
