@@ -109,6 +109,7 @@ PyObject *attn(PyObject *, PyObject *const *args, Py_ssize_t n_args) {
         }
     }
     if (packed) {
+        if (workspace && !workspace->is_contiguous()) Py_RETURN_NONE;
         if (cu->dim() != 1 || cu->size(0) < 1 || !PyLong_CheckExact(args[8])) Py_RETURN_NONE;
         const int64_t rows = cu->size(0) - 1;
         const long long longest = PyLong_AsLongLong(args[8]);

@@ -180,6 +180,8 @@ def _attn_args(kind, q, k, v, g, state, out, *, cu_seqlens=None, max_len=None, s
                 with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev) if handle
                                        else torch.cuda.default_stream(dev)):
                     workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if workspace is not None and not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
         fn, args = lib.linattn_prefill, (ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state),
                                          _ptr(slot_idx), _ptr(cu_seqlens), _ptr(has_initial_state),
@@ -304,8 +306,8 @@ def linear_attn_prefill(q, k, v, g, state, out, cu_seqlens, *, max_len: int, sca
                         slot_idx=None, has_initial_state=None, workspace=None,
                         stream=None) -> None:
     """Enqueue linear attention over packed prompts; each row's last state is left in its slot.
-    max_len >= the longest prompt.  scale: dk ** -0.5 if None.  workspace: a uint8 tensor of
-    at least the size that the shape needs (allocated here if None)."""
+    max_len >= the longest prompt.  scale: dk ** -0.5 if None.  workspace: a contiguous uint8
+    tensor of at least the size that the shape needs (allocated here if None)."""
     if stream is None and _done(_short().attn(0, q, k, v, g, state, out, cu_seqlens, max_len, scale,
                                               slot_idx, has_initial_state, None, workspace)):
         return

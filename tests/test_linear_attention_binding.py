@@ -32,3 +32,40 @@ def test_max_len_past_32_bits(m, max_len):
     with pytest.raises(ValueError, match="max_len"):
         m._attn_args("prefill", *args, cu_seqlens=cu, max_len=max_len)
     m._attn_args("prefill", *args, cu_seqlens=cu, max_len=2 ** 31 - 1)
+
+
+def _spread(size, device="cpu"):
+    """Tensors of `size` bytes by their count, over fewer or over others' between them."""
+    byte = torch.zeros(1, dtype=torch.uint8, device=device)
+    return byte.expand(size), torch.zeros(2 * size, dtype=torch.uint8, device=device)[::2]
+
+
+def test_workspace_that_is_not_whole(m):
+    """Its bytes are not where its size says: the kernels would write past or between them."""
+    args, cu = _prompt(3000)
+    lib, _, _, cargs, _ = m._attn_args("prefill", *args, cu_seqlens=cu, max_len=3000,
+                                       workspace=torch.zeros(1, dtype=torch.uint8))
+    size = lib.linattn_prefill_workspace(cargs[0])
+    assert size > 0
+    for workspace in _spread(size):
+        with pytest.raises(ValueError, match="workspace"):
+            m._attn_args("prefill", *args, cu_seqlens=cu, max_len=3000, workspace=workspace)
+    m._attn_args("prefill", *args, cu_seqlens=cu, max_len=3000, workspace=torch.zeros(size, dtype=torch.uint8))
+
+
+@pytest.mark.gpu
+def test_workspace_that_is_not_whole_both_ways():
+    """Neither way launches anything with it."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import causal_conv1d_verify_amd as cv
+
+    print("[case] workspace that is not whole", flush=True)
+    args, cu = _prompt(3000, "cuda")
+    for stream in (None, torch.cuda.current_stream()):
+        for workspace in _spread(1 << 26, "cuda"):
+            with pytest.raises(ValueError, match="workspace"):
+                cv.linear_attn_prefill(*args, cu, max_len=3000, workspace=workspace, stream=stream)
+        whole = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+        cv.linear_attn_prefill(*args, cu, max_len=3000, workspace=whole, stream=stream)
+        torch.cuda.synchronize()
