@@ -210,7 +210,9 @@ Cut cut_prompts(const la_shape_t *s, int xb, int sb, bool wide) {
     const int64_t share = std::max(kLeast, sat_mul(tokens / chunk + 1, heads) / kSlots);
     const int64_t segments = tokens / (share * chunk) + s->n_seq;
     const int64_t states = sat_mul(segments, heads);
-    if (chain > share + share / 2 && chain > 2 * kLeast && states <= INT32_MAX) {
+    // (combine's grid has one workgroup for each 4 KiB of a row's state)
+    const int64_t combines = sat_mul(sat_mul(s->n_seq, heads), c.plan.ws_bytes / 16 / c.plan.threads);
+    if (chain > share + share / 2 && chain > 2 * kLeast && states <= INT32_MAX && combines <= INT32_MAX) {
         c.seg_len = (int32_t)(share * chunk);
         c.segments = segments;
         c.ws_states = states;

@@ -33,3 +33,11 @@ def test_a_loose_bound_cuts_nothing(T, x):
 def test_a_long_row_is_cut_under_any_bound(T, x):
     tight = _workspace(2, 4000, 4000, x=x)
     assert tight > 0 and _workspace(2, 4000, T, x=x) == tight
+
+
+def test_cuts_keep_every_launch_within_a_grid():
+    """Rows times heads within a launch, times the pieces of a state not: the second of three
+    launches would be refused with the first one under way."""
+    big = dict(heads=64, dk=256, dv=256, n_slots=1)
+    assert _workspace(1 << 18, 1 << 20, 1 << 20, **big) > 0
+    assert _workspace(1 << 20, 1 << 21, 1 << 20, **big) == 0
