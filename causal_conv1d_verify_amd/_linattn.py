@@ -9,6 +9,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblinattn.
 
 LA_SILU = 0
 LA_SIGMOID = 1
+LA_CALL_PREFILL, LA_CALL_UPDATE, LA_CALL_VERIFY, LA_CALL_COMMIT = range(4)
+LA_KERNEL_TOKENS, LA_KERNEL_FEW, LA_KERNEL_CHUNKED, LA_KERNEL_CHUNKED_F32 = range(4)
 
 EXPORTS = (
     "linattn_prefill",
@@ -16,6 +18,7 @@ EXPORTS = (
     "linattn_update",
     "linattn_verify",
     "linattn_commit",
+    "linattn_describe",
     "norm_gated",
     "norm_residual",
     "linattn_strerror",
@@ -58,6 +61,15 @@ class LaNormShape(ctypes.Structure):
     ]
 
 
+class LaLaunchInfo(ctypes.Structure):
+    _fields_ = [
+        ("workgroups", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
+        ("kernel", ctypes.c_int32), ("threads", ctypes.c_int32),
+        ("state_cols", ctypes.c_int32), ("segment_tokens", ctypes.c_int32),
+        ("launches", ctypes.c_int32), ("streaming", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -80,6 +92,8 @@ def load() -> ctypes.CDLL:
         fn.restype, fn.argtypes = ctypes.c_int, args
     lib.linattn_prefill_workspace.restype = ctypes.c_int64
     lib.linattn_prefill_workspace.argtypes = [S]
+    lib.linattn_describe.restype = ctypes.c_int
+    lib.linattn_describe.argtypes = [ctypes.c_int, S, ctypes.POINTER(LaLaunchInfo)]
     lib.linattn_strerror.restype = ctypes.c_char_p
     lib.linattn_strerror.argtypes = [ctypes.c_int]
     lib.linattn_last_error.restype = ctypes.c_char_p

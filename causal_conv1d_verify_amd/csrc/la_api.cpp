@@ -165,15 +165,24 @@ laimpl::AttnArgs attn_args(const la_shape_t *s, const void *q, const void *k, co
 // 256 compute units have of the wide ones to hold two each.
 constexpr int64_t kWideBlocks = 512;
 
-int recurrent(laimpl::AttnArgs a, int xb, int sb, void *stream) {
-    laimpl::RecurrentPlan p = laimpl::pick_recurrent(xb, sb, a.dk, true);
-    int64_t heads = (int64_t)a.n_seq * a.v_heads;
-    a.tiles = (a.dv + p.cols - 1) / p.cols;
-    if (heads * a.tiles < kWideBlocks) {
-        p = laimpl::pick_recurrent(xb, sb, a.dk, false);
-        a.tiles = (a.dv + p.cols - 1) / p.cols;
+// A launch of one kernel over rows, heads and tiles of the state's columns.
+struct Plan {
+    int kernel;                   // la_kernel_t
+    const void *fn;
+    int64_t tiles, blocks;
+    int cols, threads;
+    bool streaming;
+};
+
+Plan plan_recurrent(const la_shape_t *s, int xb, int sb) {
+    laimpl::RecurrentPlan p = laimpl::pick_recurrent(xb, sb, s->dk, true);
+    const int64_t heads = (int64_t)s->n_seq * s->v_heads;
+    int64_t tiles = (s->dv + p.cols - 1) / p.cols;
+    if (heads * tiles < kWideBlocks) {
+        p = laimpl::pick_recurrent(xb, sb, s->dk, false);
+        tiles = (s->dv + p.cols - 1) / p.cols;
     }
-    return launch(p.fn, heads * a.tiles, p.threads, 0, &a, stream);
+    return {LA_KERNEL_TOKENS, p.fn, tiles, heads * tiles, p.cols, p.threads, false};
 }
 
 // How packed prompts are cut into workgroups.
@@ -249,6 +258,28 @@ int chunked(laimpl::AttnArgs a, const Cut &c, void *workspace, void *stream) {
 }
 
 // update, verify and commit
+Plan plan_few(const la_shape_t *s, const Need &need, int xb, int sb) {
+    const int64_t heads = (int64_t)s->n_seq * s->v_heads;
+    // fp32 tokens are one chunk of a prompt from 12 on, 16 without outputs (128 rows of 32 heads, verify
+    // of 8: 112 us one by one, 159 as a chunk, of 16: 205 and 162, of 32: 382 and 174; 8 rows of 16: 18
+    // and 12).
+    if (xb == 4 && s->T >= (need.out ? 12 : 16) && in_chunks(s)) {
+        const laimpl::ChunkedPlan p = laimpl::pick_chunked_f32(s->dk);
+        const int64_t tiles = (s->dv + p.cols - 1) / p.cols;
+        return {LA_KERNEL_CHUNKED_F32, p.run, tiles, heads * tiles, p.cols, p.threads, false};
+    }
+    // On the matrix cores where tokens are bf16, single ones only where the state's traffic counts
+    // (256 rows of 32 heads: 184 us for 197); for few workgroups the recurrence starts sooner (one row
+    // of 48 heads: 4.4 us for 6.5).
+    const int64_t tiles = (s->dv + 127) / 128;
+    if (xb == 4 || (s->T == 1 && heads * tiles < kWideBlocks)) return plan_recurrent(s, xb, sb);
+    return {LA_KERNEL_FEW, laimpl::pick_few(sb, s->dk, s->T, need.out, !need.verify), tiles, heads * tiles, 128, 256,
+            past_caches(sat_mul(heads, (int64_t)s->dk * s->dv * sb))};
+}
+
+constexpr Need kNeeds[] = {{true, true, true, false}, {true, true, false, false}, {true, true, false, true},
+                           {false, false, false, false}};   // by la_call_t
+
 int few_tokens(const la_shape_t *s, const Need &need, const void *q, const void *k, const void *v, const float *g,
                const void *state, const int32_t *slot_idx, const int32_t *num_tokens, void *out, void *stream) {
     g_detail[0] = 0;
@@ -263,24 +294,12 @@ int few_tokens(const la_shape_t *s, const Need &need, const void *q, const void 
                           {"slot_idx", slot_idx, false, 4}, {"num_tokens", num_tokens, false, 4}};
     if ((rc = check_pointers(ps)) != CV_OK) return rc;
     laimpl::AttnArgs a = attn_args(s, q, k, v, g, state, slot_idx, nullptr, num_tokens, nullptr, out, !need.verify);
-    // On the matrix cores where tokens are bf16, single ones only where the state's traffic counts
-    // (256 rows of 32 heads: 184 us for 197); for few workgroups the recurrence starts sooner (one row
-    // of 48 heads: 4.4 us for 6.5).
-    a.tiles = (s->dv + 127) / 128;
-    const int64_t blocks = (int64_t)s->n_seq * s->v_heads * a.tiles;
-    a.streaming = past_caches(sat_mul((int64_t)s->n_seq * s->v_heads, (int64_t)s->dk * s->dv * sb));
-    // fp32 tokens are one chunk of a prompt from 12 on, 16 without outputs (128 rows of 32 heads, verify
-    // of 8: 112 us one by one, 159 as a chunk, of 16: 205 and 162, of 32: 382 and 174; 8 rows of 16: 18
-    // and 12).
-    if (xb == 4 && s->T >= (need.out ? 12 : 16) && in_chunks(s)) {
-        const laimpl::ChunkedPlan p = laimpl::pick_chunked_f32(s->dk);
-        a.tiles = (s->dv + p.cols - 1) / p.cols;
-        a.seg_len = s->T;
-        a.segments = s->n_seq;
-        return launch(p.run, (int64_t)s->n_seq * s->v_heads * a.tiles, p.threads, 0, &a, stream);
-    }
-    if (xb == 4 || (s->T == 1 && blocks < kWideBlocks)) return recurrent(a, xb, sb, stream);
-    return launch(laimpl::pick_few(sb, s->dk, s->T, need.out, !need.verify), blocks, 256, 0, &a, stream);
+    const Plan p = plan_few(s, need, xb, sb);
+    a.tiles = (int32_t)p.tiles;
+    a.streaming = p.streaming;
+    a.seg_len = s->T;                              // a row is one segment (LA_KERNEL_CHUNKED_F32)
+    a.segments = s->n_seq;
+    return launch(p.fn, p.blocks, p.threads, 0, &a, stream);
 }
 
 int check_norm(const la_norm_shape_t *s, bool residual, int *xb, int *rb) {
@@ -323,7 +342,7 @@ int64_t linattn_prefill_workspace(const la_shape_t *s) {
     g_detail[0] = 0;
     int xb, sb;
     bool empty;
-    const int rc = check_attn(s, Need{true, true, true, false}, &xb, &sb, &empty);
+    const int rc = check_attn(s, kNeeds[LA_CALL_PREFILL], &xb, &sb, &empty);
     if (rc != CV_OK || empty || !in_chunks(s)) return rc;
     return cut_prompts(s, xb, sb).ws_bytes;
 }
@@ -345,25 +364,60 @@ int linattn_prefill(const la_shape_t *s, const void *q, const void *k, const voi
                           {"slot_idx", slot_idx, false, 4}, {"has_initial_state", has_initial_state, false, 4}};
     if ((rc = check_pointers(ps)) != CV_OK) return rc;
     const int xb = dtype_bytes(s->x_dtype), sb = dtype_bytes(s->state_dtype);
-    const laimpl::AttnArgs a = attn_args(s, q, k, v, g, state, slot_idx, cu_seqlens, nullptr, has_initial_state, out, true);
-    if (!in_chunks(s)) return recurrent(a, xb, sb, hip_stream);
+    laimpl::AttnArgs a = attn_args(s, q, k, v, g, state, slot_idx, cu_seqlens, nullptr, has_initial_state, out, true);
+    if (!in_chunks(s)) {
+        const Plan p = plan_recurrent(s, xb, sb);
+        a.tiles = (int32_t)p.tiles;
+        return launch(p.fn, p.blocks, p.threads, 0, &a, hip_stream);
+    }
     return chunked(a, cut_prompts(s, xb, sb), workspace, hip_stream);
 }
 
 int linattn_update(const la_shape_t *s, const void *q, const void *k, const void *v, const float *g, void *state,
                    const int32_t *slot_idx, void *out, void *hip_stream) {
-    return few_tokens(s, Need{true, true, false, false}, q, k, v, g, state, slot_idx, nullptr, out, hip_stream);
+    return few_tokens(s, kNeeds[LA_CALL_UPDATE], q, k, v, g, state, slot_idx, nullptr, out, hip_stream);
 }
 
 int linattn_verify(const la_shape_t *s, const void *q, const void *k, const void *v, const float *g,
                    const void *state, const int32_t *slot_idx, void *out, void *hip_stream) {
-    return few_tokens(s, Need{true, true, false, true}, q, k, v, g, state, slot_idx, nullptr, out, hip_stream);
+    return few_tokens(s, kNeeds[LA_CALL_VERIFY], q, k, v, g, state, slot_idx, nullptr, out, hip_stream);
 }
 
 int linattn_commit(const la_shape_t *s, const void *k, const void *v, const float *g, void *state,
                    const int32_t *slot_idx, const int32_t *num_tokens, void *hip_stream) {
-    return few_tokens(s, Need{false, false, false, false}, nullptr, k, v, g, state, slot_idx, num_tokens, nullptr,
+    return few_tokens(s, kNeeds[LA_CALL_COMMIT], nullptr, k, v, g, state, slot_idx, num_tokens, nullptr,
                       hip_stream);
+}
+
+int linattn_describe(int call, const la_shape_t *s, la_launch_info_t *info) {
+    g_detail[0] = 0;
+    if (call < LA_CALL_PREFILL || call > LA_CALL_COMMIT) return fail(CV_EINVAL, "unknown call %d", call);
+    if (!info) return fail(CV_EINVAL, "info is NULL");
+    int xb, sb;
+    bool empty;
+    const Need &need = kNeeds[call];
+    const int rc = check_attn(s, need, &xb, &sb, &empty);
+    if (rc != CV_OK) return rc;
+    *info = la_launch_info_t{};
+    if (empty) return CV_OK;
+    info->launches = 1;
+    if (need.packed && in_chunks(s)) {
+        const Cut c = cut_prompts(s, xb, sb);
+        info->kernel = xb == 4 ? LA_KERNEL_CHUNKED_F32 : LA_KERNEL_CHUNKED;
+        info->workgroups = c.segments * s->v_heads * c.tiles;
+        info->threads = c.plan.threads;
+        info->state_cols = c.plan.cols;
+        info->workspace_bytes = c.ws_bytes;
+        if (c.ws_states) info->launches = 3, info->segment_tokens = c.seg_len;
+        return CV_OK;
+    }
+    const Plan p = need.packed ? plan_recurrent(s, xb, sb) : plan_few(s, need, xb, sb);
+    info->kernel = p.kernel;
+    info->workgroups = p.blocks;
+    info->threads = p.threads;
+    info->state_cols = p.cols;
+    info->streaming = p.streaming;
+    return CV_OK;
 }
 
 int norm_gated(const la_norm_shape_t *s, const void *y, const void *gate, const void *weight, void *out,

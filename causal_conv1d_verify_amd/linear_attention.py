@@ -32,8 +32,8 @@ import ctypes
 from . import _lib, _linattn
 
 __all__ = ["linear_attn_prefill", "linear_attn_update", "linear_attn_verify",
-           "linear_attn_commit", "gated_norm", "residual_norm", "linear_attn_abi_version",
-           "LinAttnError"]
+           "linear_attn_commit", "gated_norm", "residual_norm", "linear_attn_describe",
+           "linear_attn_abi_version", "LinAttnError"]
 
 ACTIVATIONS = {"silu": _linattn.LA_SILU, "sigmoid": _linattn.LA_SIGMOID}
 
@@ -392,6 +392,18 @@ def prepared(kind, args, kwargs):
 
     launch.keepalive = keep
     return launch
+
+
+def linear_attn_describe(call, *args, **kwargs) -> "_linattn.LaLaunchInfo":
+    """How a call with these arguments is launched (host only; raises what the call raises).
+    call: "prefill", "update", "verify" or "commit", with the arguments of that entry point."""
+    lib, _dev, _fn, cargs, _keep = PREPARE["linear_attn_" + call](*args, **kwargs)
+    info = _linattn.LaLaunchInfo()
+    code = ("prefill", "update", "verify", "commit").index(call)
+    rc = lib.linattn_describe(code, cargs[0], ctypes.byref(info))
+    if rc != _lib.CV_OK:
+        raise LinAttnError(rc, _linattn.error_message(lib, rc))
+    return info
 
 
 def linear_attn_abi_version() -> int:

@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define LINEAR_ATTENTION_ABI_VERSION 1
+#define LINEAR_ATTENTION_ABI_VERSION 2
 
 typedef struct la_shape {
     int32_t n_seq;        /* rows, >= 0 (0: nothing to do)                                  */
@@ -113,6 +113,28 @@ CV_API int linattn_verify(const la_shape_t *shape, const void *q, const void *k,
 CV_API int linattn_commit(const la_shape_t *shape, const void *k, const void *v, const float *g,
                           void *state, const int32_t *slot_idx, const int32_t *num_tokens,
                           void *hip_stream);
+
+/* How a call of this shape is launched (host only; nothing is launched). */
+typedef enum la_call {
+    LA_CALL_PREFILL = 0, LA_CALL_UPDATE = 1, LA_CALL_VERIFY = 2, LA_CALL_COMMIT = 3
+} la_call_t;
+typedef enum la_kernel {
+    LA_KERNEL_TOKENS = 0,        /* token by token                                          */
+    LA_KERNEL_FEW = 1,           /* up to 32 bf16 tokens in one pass over the state         */
+    LA_KERNEL_CHUNKED = 2,       /* bf16 tokens in chunks of 64                             */
+    LA_KERNEL_CHUNKED_F32 = 3    /* fp32 tokens in chunks of 32                             */
+} la_kernel_t;
+typedef struct la_launch_info {
+    int64_t workgroups;     /* of the launch that makes the outputs (the states)            */
+    int64_t workspace_bytes;
+    int32_t kernel;         /* la_kernel_t                                                  */
+    int32_t threads;        /* of a workgroup                                               */
+    int32_t state_cols;     /* columns of a state in a workgroup                            */
+    int32_t segment_tokens; /* prompts: tokens of a segment of a cut row; 0: none is cut    */
+    int32_t launches;       /* 3 where rows are cut, 0 where there is nothing to do         */
+    int32_t streaming;      /* 1: the states' loads and stores go past the caches           */
+} la_launch_info_t;
+CV_API int linattn_describe(int call, const la_shape_t *shape, la_launch_info_t *info);
 
 /* Gate activations of norm_gated. */
 typedef enum la_act { LA_SILU = 0, LA_SIGMOID = 1 } la_act_t;
