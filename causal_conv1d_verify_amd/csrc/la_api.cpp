@@ -199,7 +199,7 @@ Plan plan_recurrent(const la_shape_t *s, int xb, int sb) {
 // generation of workgroups (8 rows of up to 160 tokens, 48 heads: 21 us for 27).
 struct Cut {
     laimpl::ChunkedPlan plan;
-    int64_t tiles, segments, ws_states, ws_bytes;
+    int64_t tiles, segments, places, ws_states, ws_bytes;
     int32_t seg_len;
 };
 Cut cut_prompts(const la_shape_t *s, int xb, int sb, bool wide) {
@@ -224,8 +224,10 @@ Cut cut_prompts(const la_shape_t *s, int xb, int sb, bool wide) {
     if (chain > share + share / 2 && chain > 2 * kLeast && states <= INT32_MAX && combines <= INT32_MAX) {
         c.seg_len = (int32_t)(share * chunk);
         c.segments = segments;
-        c.ws_states = states;
-        c.ws_bytes = sat_add(sat_mul(states, c.plan.ws_bytes), (4 * states + 15) / 16 * 16);
+        // only rows of more than seg_len tokens have places in the workspace
+        c.places = tokens / c.seg_len + std::min<int64_t>(s->n_seq, tokens / c.seg_len);
+        c.ws_states = c.places * heads;
+        c.ws_bytes = sat_add(sat_mul(c.ws_states, c.plan.ws_bytes), (4 * c.ws_states + 15) / 16 * 16);
     }
     if (wide && (c.segments * heads <= 128 || (chain <= 4 && c.segments * heads <= kSlots))) return cut_prompts(s, xb, sb, false);
     return c;
@@ -243,6 +245,7 @@ int chunked(laimpl::AttnArgs a, const Cut &c, void *workspace, void *stream) {
     a.tiles = (int32_t)c.tiles;
     a.seg_len = c.seg_len;
     a.segments = (int32_t)c.segments;
+    a.places = (int32_t)c.places;
     a.ws = workspace;
     a.ws_total = reinterpret_cast<float *>(static_cast<char *>(workspace) + c.ws_states * c.plan.ws_bytes);
     const int64_t blocks = c.segments * a.v_heads * c.tiles;

@@ -54,7 +54,7 @@ struct Shared {
     union __attribute__((aligned(16))) { char q[C * QP]; char p[2][C * PP]; };
     __attribute__((aligned(16))) char k[C * KP], v[C * VP], zeros[16];
     Decays d[2];
-    int64_t found[2];
+    int64_t found[3];
 };
 
 // KT: dk in blocks of 32; W: wavefronts; NC: column tiles of 16 of each; OUT: outputs are wanted, else
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, g4 = 4 * (lane >> 4);
     int rest = shared_block(blockIdx.x, a.group * a.tiles, gridDim.x);
-    const int tile = rest % a.tiles;
+    const int tile = uniform(rest % a.tiles);
     rest /= a.tiles;
     const int h = uniform(rest % a.v_heads), id = uniform(rest / a.v_heads);
     const int hq = h / a.group;
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(64 * W, KT <= 4 || NC == 1 ? 2 : 1) void chunked(co
         }
         return f;
     };
-    const int64_t ws_head = ((int64_t)id * a.v_heads + h) * a.tiles + tile;
+    const int64_t ws_head = ((int64_t)(seg.place + seg.index) * a.v_heads + h) * a.tiles + tile;
     const int64_t ws_step = (int64_t)a.v_heads * a.tiles;          // from segment to segment
     constexpr int64_t WS = (int64_t)64 * W * NC * DT;              // f32x4 of one workgroup
     f32x4 S[NC][DT];
@@ -547,9 +547,9 @@ __global__ __launch_bounds__(64 * W) void combine(const AttnArgs a, const int ve
     const int ht = rest % (a.v_heads * a.tiles), i = rest / (a.v_heads * a.tiles);
     const int count = uniform(segments_of(a, i));
     if (count < 2) return;                         // same for the workgroup
-    const int64_t id = first_segment<W>(a, i);
-    if (id + count > a.segments) return;
-    const int64_t step = (int64_t)a.v_heads * a.tiles, at = id * step + ht;
+    const int64_t place = first_place<W>(a, i);
+    if (place + count > a.places) return;
+    const int64_t step = (int64_t)a.v_heads * a.tiles, at = place * step + ht;
     f32x4 *w = static_cast<f32x4 *>(a.ws) + at * vectors + part * (64 * W) + threadIdx.x;
     const float *total = a.ws_total + at;
     f32x4 S = w[(count - 1) * step * vectors];

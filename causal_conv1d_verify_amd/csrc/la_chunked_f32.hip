@@ -25,7 +25,7 @@ struct Shared {
     static constexpr int QP = DT * 16 + 4, PP = C + 4;             // floats of a row
     __attribute__((aligned(16))) float q[C * QP], k[C * QP], p[C * PP];
     Decays32 d[2];
-    int64_t found[2];
+    int64_t found[3];
 };
 
 // DT: row tiles of 16; OUT as in la_chunked.hip.
@@ -37,7 +37,7 @@ __global__ __launch_bounds__(64 * W, 2) void chunked_f32(const AttnArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int j = lane & 15, g4 = 4 * (lane >> 4);
     int rest = blockIdx.x;
-    const int tile = rest % a.tiles;
+    const int tile = uniform(rest % a.tiles);
     rest /= a.tiles;
     const int h = uniform(rest % a.v_heads), id = uniform(rest / a.v_heads);
     const int hq = h / a.group;
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(64 * W, 2) void chunked_f32(const AttnArgs a) {
         }
         return f;
     };
-    const int64_t ws_head = ((int64_t)id * a.v_heads + h) * a.tiles + tile;
+    const int64_t ws_head = ((int64_t)(seg.place + seg.index) * a.v_heads + h) * a.tiles + tile;
     const int64_t ws_step = (int64_t)a.v_heads * a.tiles;
     constexpr int64_t WS = (int64_t)64 * W * DT;
     f32x4 S[DT];

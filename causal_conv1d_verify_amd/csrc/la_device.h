@@ -149,51 +149,54 @@ __device__ __forceinline__ void store_one(Bf16 *p, float x) {
 
 // Segment `id` of the rows in order, each row cut into ceil(tokens / seg_len) of them and one
 // where it has no tokens; row -1 where there are fewer.  Rows that are skipped have none, nor
-// has a row that would end past a.segments (more tokens than the caller declared).  Called by
-// a whole workgroup of W wavefronts, `shared` is two words of LDS.
-struct Segment { int row, index; bool last; };
+// has a row that would end past a.segments or a.places (more tokens than the caller declared).
+// `place` is the row's first place in the workspace, where rows of one segment have none.  Called
+// by a whole workgroup of W wavefronts, `shared` is three words of LDS.
+struct Segment { int row, index; bool last; int place; };
 __device__ __forceinline__ int segments_of(const AttnArgs &a, int i) {
     const Row r = row_of(a, i);
     return r.n < 0 ? 0 : r.n == 0 ? 1 : (int)(((uint32_t)r.n + (uint32_t)a.seg_len - 1) / (uint32_t)a.seg_len);
 }
+__device__ __forceinline__ int places_of(int segments) { return segments > 1 ? segments : 0; }
 template <int W>
 __device__ __forceinline__ Segment find_segment(const AttnArgs &a, int id, int64_t *shared) {
-    if (a.seg_len >= a.T) return row_of(a, id).n < 0 ? Segment{-1, 0, true} : Segment{id, 0, true};
-    __shared__ int sums[W];
+    if (a.seg_len >= a.T) return row_of(a, id).n < 0 ? Segment{-1, 0, true, 0} : Segment{id, 0, true, 0};
+    __shared__ int sums[2][W];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t before = 0;                            // segments of the rows before these
+    int64_t before = 0, places = 0;                // of the rows before these
     if (threadIdx.x == 0) shared[0] = -1;
     for (int i0 = 0; i0 < a.n_seq && before <= id; i0 += 64 * W) {
         const int i = i0 + threadIdx.x;
-        const int own = i < a.n_seq ? segments_of(a, i) : 0;
-        int upto = own;
+        const int own = i < a.n_seq ? segments_of(a, i) : 0, held = places_of(own);
+        int upto = own, held_upto = held;
 #pragma unroll
         for (int d = 1; d < kWave; d *= 2) {
-            const int y = __shfl_up(upto, d);
-            if (lane >= d) upto += y;
+            const int y = __shfl_up(upto, d), z = __shfl_up(held_upto, d);
+            if (lane >= d) upto += y, held_upto += z;
         }
         __syncthreads();                           // the sums of the last turn are read
-        if (lane == kWave - 1) sums[wave] = upto;
+        if (lane == kWave - 1) sums[0][wave] = upto, sums[1][wave] = held_upto;
         __syncthreads();
-        int64_t at = before + upto - own;
-        for (int w = 0; w < wave; ++w) at += sums[w];
-        if (id >= at && id < at + own && at + own <= a.segments) {
+        int64_t at = before + upto - own, place = places + held_upto - held;
+        for (int w = 0; w < wave; ++w) at += sums[0][w], place += sums[1][w];
+        if (id >= at && id < at + own && at + own <= a.segments && place + held <= a.places) {
             shared[0] = i;
             shared[1] = (id - at) * 2 + (id - at == own - 1);
+            shared[2] = place;
         }
-        for (int w = 0; w < W; ++w) before += sums[w];
+        for (int w = 0; w < W; ++w) before += sums[0][w], places += sums[1][w];
     }
     __syncthreads();
     const int64_t at = uniform(shared[1]);
-    return Segment{uniform((int)shared[0]), (int)(at >> 1), (at & 1) != 0};
+    return Segment{uniform((int)shared[0]), (int)(at >> 1), (at & 1) != 0, uniform((int)shared[2])};
 }
 
-// The number of row i's first segment (i the same for the workgroup).
+// The first place of row i in the workspace (i the same for the workgroup).
 template <int W>
-__device__ __forceinline__ int64_t first_segment(const AttnArgs &a, int i) {
+__device__ __forceinline__ int64_t first_place(const AttnArgs &a, int i) {
     __shared__ int64_t sums[W];
     int64_t own = 0;
-    for (int r = threadIdx.x; r < i; r += 64 * W) own += segments_of(a, r);
+    for (int r = threadIdx.x; r < i; r += 64 * W) own += places_of(segments_of(a, r));
 #pragma unroll
     for (int d = kWave / 2; d > 0; d /= 2) own += __shfl_xor(own, d);
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = own;

@@ -31,7 +31,8 @@ struct AttnArgs {
     int32_t streaming;            // the states of this call are more than the caches keep
     // prompts in chunks: a row is cut into segments of seg_len tokens (a multiple of the chunk;
     // rows of at most seg_len tokens are one)
-    int32_t seg_len, segments;          // segments that the grid and the workspace hold
+    int32_t seg_len, segments;          // segments that the grid holds
+    int32_t places;                     // segments of cut rows that the workspace holds
     void *ws;                           // what each segment adds to a state (a row's last: the row's
                                         // first state), then the state behind it
     float *ws_total;                    // the decay over each

@@ -41,3 +41,17 @@ def test_cuts_keep_every_launch_within_a_grid():
     big = dict(heads=64, dk=256, dv=256, n_slots=1)
     assert _workspace(1 << 18, 1 << 20, 1 << 20, **big) > 0
     assert _workspace(1 << 20, 1 << 21, 1 << 20, **big) == 0
+
+
+@pytest.mark.parametrize("x", [base.CV_BF16, base.CV_F32])
+def test_rows_that_are_not_cut_take_no_workspace(x):
+    """A long prompt among short ones: all tokens together make at most 512 segments of a head's tile,
+    and cut rows' last ones as many again, however many rows there are."""
+    heads, dk, dv = 48, 128, 128
+    most = 2 * 512 * dk * dv * 4                 # tiles of 128 columns at most
+
+    def need(n_seq, tokens):
+        return _workspace(n_seq, tokens, 16384, heads=heads, dk=dk, dv=dv, x=x)
+
+    assert 0 < need(1, 16384) <= need(256, 16384 + 255 * 160) <= most + 8192
+    assert need(20000, 16384 + 19999) <= most + 8192
