@@ -88,7 +88,8 @@ def _run(cmd):
 
 def build(verbose: bool = True) -> str:
     """Builds libconvverify.so, the write-count test library libconvverify_wc.so, liblinattn.so
-    and _lacall.so."""
+    and _lacall.so.  Only the last needs Python's and torch's headers: where it cannot be built the
+    libraries are there all the same, and the error is raised behind them."""
     os.makedirs(os.path.join(BUILD, "wc"), exist_ok=True)
     t0 = time.time()
     pending = []
@@ -99,15 +100,22 @@ def build(verbose: bool = True) -> str:
             obj = os.path.join(BUILD, stem + ".o")
             pending.append([HIPCC, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
             objs.append(obj)
-        libs.append((lib, objs, []))
-    compile_call, link_call = _call_module()
-    call_obj = os.path.join(BUILD, "la_call.o")
-    pending.insert(0, [HIPCC, *COMMON, *compile_call, "-c", os.path.join(CSRC, "la_call.cpp"), "-o", call_obj])
-    libs.append((LIB_CALL, [call_obj], link_call))
+        libs.append((lib, objs))
+    call_obj, call_cmd, call_error = os.path.join(BUILD, "la_call.o"), None, None
+    try:
+        compile_call, link_call = _call_module()
+        call_cmd = [HIPCC, *COMMON, *compile_call, "-c", os.path.join(CSRC, "la_call.cpp"), "-o", call_obj]
+        pending.insert(0, call_cmd)
+    except Exception as e:
+        call_error = e
     running = []
 
     def reap(cmd, p):
+        nonlocal call_error
         out, err = p.communicate()
+        if p.returncode != 0 and cmd is call_cmd:
+            call_error = RuntimeError(f"build step failed ({p.returncode}):\n{' '.join(cmd)}\n{out}\n{err}")
+            return
         if p.returncode != 0:
             for _, q in running:
                 q.kill()
@@ -124,10 +132,22 @@ def build(verbose: bool = True) -> str:
                                                   stderr=subprocess.PIPE, text=True)))
         cmd, p = running.pop(0)
         reap(cmd, p)
-    for lib, objs, link in libs:
+
+    def link(lib, objs, flags=()):
         tmp = lib + ".tmp"
-        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, *link, "-o", tmp])
+        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, *flags, "-o", tmp])
         os.replace(tmp, lib)
+
+    for lib, objs in libs:
+        link(lib, objs)
+    try:
+        if call_error is not None:
+            raise call_error
+        link(LIB_CALL, [call_obj], link_call)
+    except Exception:
+        if os.path.exists(LIB_CALL):               # an older one's view of the library may be another
+            os.remove(LIB_CALL)
+        raise
     if verbose:
         print(f"built {LIB}, {LIB_WC}, {LIB_LA} and {LIB_CALL} in {time.time() - t0:.1f}s", file=sys.stderr)
     return LIB
