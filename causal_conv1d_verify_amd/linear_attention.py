@@ -282,14 +282,32 @@ def _issue(lib, dev, fn, args, keep):
 _call = None
 
 
+class _NoCallModule:
+    """In the call module's place: every call takes the binding's own way."""
+
+    @staticmethod
+    def attn(*args):
+        return None
+
+    gated = residual = attn
+
+
 def _short():
     """The call module (csrc/la_call.cpp): the same marshalling in C for calls that are plainly in
-    order; it answers None to all others, and they take the way above."""
+    order; it answers None to all others, and they take the way above, as all do without it (it is
+    built for one torch and one Python, and the library under both ways is not)."""
     global _call
     if _call is None:
         import torch  # noqa: F401  (its libraries, which the module is linked to)
 
-        from . import _lacall as _call
+        try:
+            from . import _lacall as _call
+        except ImportError as e:
+            import warnings
+
+            _call = _NoCallModule
+            warnings.warn(f"calls are marshalled in Python, some 12 us each slower: {e} (build it with "
+                          "`python -m causal_conv1d_verify_amd.build`)", RuntimeWarning, stacklevel=3)
     return _call
 
 
