@@ -190,13 +190,14 @@ Plan plan_recurrent(const la_shape_t *s, int xb, int sb) {
 // Along a row: its tokens are one chain of chunks in one workgroup unless that chain is much
 // longer than the share of all chunks that each of the chip's slots would have (two workgroups on
 // each of 256 compute units): then rows are cut into segments of about that share, at the price
-// of passing over their k and v twice (one prompt of 16384 with 32 heads: 192 us in 16
-// segments).
+// of passing over their k and v twice (one prompt of 16384 with 32 heads: 857 us uncut, 194-199 in
+// 16 segments; 5 of up to 777 fp32 tokens with 6 heads of 96 x 72: 91 us uncut, 36 in segments of 128).
 //
 // Across a head (bf16 tokens; fp32 ones go in tiles of 64): tiles of 128 columns, since what a
-// chunk reads and the products q.k serve all of a tile; tiles of 64 where the wide ones would leave most compute units empty (64 workgroups of
-// 32 chunks: 122 us for 160) or the state's way in and out counts, in a few chunks of one
-// generation of workgroups (8 rows of up to 160 tokens, 48 heads: 21 us for 27).
+// chunk reads and the products q.k serve all of a tile; tiles of 64 where the wide ones would leave
+// most compute units empty (64 workgroups of 32 chunks: 122 us for 160) or the state's way in and
+// out counts, in a few chunks of one generation of workgroups (8 rows of up to 160 tokens, 48
+// heads: 21 us for 27).
 struct Cut {
     laimpl::ChunkedPlan plan;
     int64_t tiles, segments, places, ws_states, ws_bytes;
@@ -271,9 +272,10 @@ Plan plan_few(const la_shape_t *s, const Need &need, int xb, int sb) {
         const int64_t tiles = (s->dv + p.cols - 1) / p.cols;
         return {LA_KERNEL_CHUNKED_F32, p.run, tiles, heads * tiles, p.cols, p.threads, false};
     }
-    // On the matrix cores where tokens are bf16, single ones only where the state's traffic counts
-    // (256 rows of 32 heads: 184 us for 197); for few workgroups the recurrence starts sooner (one row
-    // of 48 heads: 4.4 us for 6.5).
+    // On the matrix cores where tokens are bf16, single ones from 512 workgroups on (256 rows of 32
+    // heads: 184 us for 197 by the recurrence); for few workgroups the recurrence starts sooner (one row
+    // of 48 heads: 4.4 us for 6.5).  The two meet later than here: 12 rows of 48 heads, 576 workgroups,
+    // take 16.9 us for 13.1, 30 rows 36.2 for 35.6.
     const int64_t tiles = (s->dv + 127) / 128;
     if (xb == 4 || (s->T == 1 && heads * tiles < kWideBlocks)) return plan_recurrent(s, xb, sb);
     return {LA_KERNEL_FEW, laimpl::pick_few(sb, s->dk, s->T, need.out, !need.verify), tiles, heads * tiles, 128, 256,

@@ -19,17 +19,17 @@
 // in LDS are padded by 32 bytes (k, v), which both ways of reading take at their full rate (5 cycles an
 // instruction, where rows of 256 bytes take 16 to 32), or by 16 (q, the products), which 8-byte reads do.
 //
-// Measured: 8 prompts of 2048 tokens with 48 heads of 128 x 128 (fp32 state) 216 us; one of 16384
-// with 32 heads in 16 segments (bf16 state) 194 us, 60 of them the segments' own states and 14 their
+// Measured: 8 prompts of 2048 tokens with 48 heads of 128 x 128 (fp32 state) 211-216 us; one of 16384
+// with 32 heads in 16 segments (bf16 state) 194-199 us, 58 of them the segments' own states and 13 their
 // sums.  What bounds it: the traffic (565 MB) would take 94 us, and the matrix instructions that the
-// parts make of it (a wavefront's 229 of 16 cycles a chunk) about 100; a chunk of two workgroups on a
-// compute unit takes 13,000 cycles, in which one wavefront's 600 vector instructions, at 4 to 5
-// cycles each, and its matrix instructions share the issue with the other's, and the clock goes from
-// 2.4 GHz with a few workgroups to 1.6-1.8 GHz with all of them.  Tried and slower: 8 wavefronts of
-// 16 columns (288 for 238 us at the time), tiles of 64 columns on a full chip (231 for 213), one
-// XCD's blocks contiguous.  Without effect: priorities, the compiler's order inside steps, loads and
-// stores past the caches.  Two parts instead of three for an fp32 state's values would save 9%, at
-// 2^-18 of each token's contribution for 2^-24.
+// parts make of it (a wavefront's 230 of 16 cycles a chunk) about 100; a chunk of two workgroups on a
+// compute unit takes 13,000 cycles (12,000 alone), the matrix units busy for 42% of them: one
+// wavefront's 560 vector instructions, at 4 to 5 cycles each, and its matrix instructions share the
+// issue with the other's, and the clock goes from 2.4 GHz with a few workgroups to 1.9 with all of
+// them.  Tried and slower: 8 wavefronts of 16 columns (288 for 238 us at the time), tiles of 64
+// columns on a full chip (231 for 213), one XCD's blocks contiguous.  Without effect: priorities, the
+// compiler's order inside steps, loads and stores past the caches.  Two parts instead of three for an
+// fp32 state's values would save 9%, at 2^-18 of each token's contribution for 2^-24.
 #include <type_traits>
 
 #include "la_matrix.h"

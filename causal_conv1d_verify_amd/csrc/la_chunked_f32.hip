@@ -1,10 +1,13 @@
-// Packed prompts of fp32 tokens (and 12 to 32 tokens of each row, as one chunk), in chunks of 32: the formulas and the division of la_chunked.hip
-// with fp32 products of 16 x 16 x 4, so no factor is taken apart.  A wavefront owns 16 of the
-// state's columns over all dk rows in registers, and its four rows of a register group are four
-// places of the product with q, read 16 bytes a lane.  v goes from memory to the lanes that use it.
-// Bound by the fp32 matrix rate (a sixteenth of bf16's), of which the state's two products take the
-// most, and at few rows by the length of a chain.  Measured: 5 prompts of up to 777 tokens, 6 heads of
-// 96 x 72, in segments of 128: 37 us (12 + 5 + 21 in its three kernels).
+// Packed prompts of fp32 tokens (and 12 to 32 tokens of each row, as one chunk), in chunks of 32: the
+// formulas and the division of la_chunked.hip with fp32 products of 16 x 16 x 4, so no factor is taken
+// apart.  A wavefront owns 16 of the state's columns over all dk rows in registers, and its four rows
+// of a register group are four places of the product with q, read 16 bytes a lane.  v goes from memory
+// to the lanes that use it.  Measured: 5 prompts of up to 777 tokens, 6 heads of 96 x 72, in segments
+// of 128: 36 us (12 + 5 + 21 in its three kernels, traced).  What bounds it there is the length of a
+// chain, four chunks of some 5 us in few workgroups: the matrix units are busy for a third of a
+// wavefront's time, and in the tile past column 64 one wavefront of four has columns (8).  With the
+// card full the fp32 matrix rate (a sixteenth of bf16's) would be the bound; the state's two products
+// take the most of it.
 #include "la_matrix.h"
 
 namespace laimpl {
