@@ -178,11 +178,11 @@ Plan plan_recurrent(const la_shape_t *s, int xb, int sb) {
     laimpl::RecurrentPlan p = laimpl::pick_recurrent(xb, sb, s->dk, true);
     const int64_t heads = (int64_t)s->n_seq * s->v_heads;
     int64_t tiles = (s->dv + p.cols - 1) / p.cols;
-    if (heads * tiles < kWideBlocks) {
+    if (sat_mul(heads, tiles) < kWideBlocks) {
         p = laimpl::pick_recurrent(xb, sb, s->dk, false);
         tiles = (s->dv + p.cols - 1) / p.cols;
     }
-    return {LA_KERNEL_TOKENS, p.fn, tiles, heads * tiles, p.cols, p.threads, false};
+    return {LA_KERNEL_TOKENS, p.fn, tiles, sat_mul(heads, tiles), p.cols, p.threads, false};
 }
 
 // How packed prompts are cut into workgroups.
@@ -230,7 +230,8 @@ Cut cut_prompts(const la_shape_t *s, int xb, int sb, bool wide) {
         c.ws_states = c.places * heads;
         c.ws_bytes = sat_add(sat_mul(c.ws_states, c.plan.ws_bytes), (4 * c.ws_states + 15) / 16 * 16);
     }
-    if (wide && (c.segments * heads <= 128 || (chain <= 4 && c.segments * heads <= kSlots))) return cut_prompts(s, xb, sb, false);
+    const int64_t blocks = sat_mul(c.segments, heads);
+    if (wide && (blocks <= 128 || (chain <= 4 && blocks <= kSlots))) return cut_prompts(s, xb, sb, false);
     return c;
 }
 Cut cut_prompts(const la_shape_t *s, int xb, int sb) { return cut_prompts(s, xb, sb, xb == 2 && s->dv > 64); }
@@ -249,7 +250,7 @@ int chunked(laimpl::AttnArgs a, const Cut &c, void *workspace, void *stream) {
     a.places = (int32_t)c.places;
     a.ws = workspace;
     a.ws_total = reinterpret_cast<float *>(static_cast<char *>(workspace) + c.ws_states * c.plan.ws_bytes);
-    const int64_t blocks = c.segments * a.v_heads * c.tiles;
+    const int64_t blocks = sat_mul(c.segments, a.v_heads * c.tiles);
     if (c.ws_states) {
         int rc = launch(c.plan.first, blocks, c.plan.threads, 0, &a, stream);
         if (rc != CV_OK) return rc;
@@ -270,15 +271,15 @@ Plan plan_few(const la_shape_t *s, const Need &need, int xb, int sb) {
     if (xb == 4 && s->T >= (need.out ? 12 : 16) && in_chunks(s)) {
         const laimpl::ChunkedPlan p = laimpl::pick_chunked_f32(s->dk);
         const int64_t tiles = (s->dv + p.cols - 1) / p.cols;
-        return {LA_KERNEL_CHUNKED_F32, p.run, tiles, heads * tiles, p.cols, p.threads, false};
+        return {LA_KERNEL_CHUNKED_F32, p.run, tiles, sat_mul(heads, tiles), p.cols, p.threads, false};
     }
     // On the matrix cores where tokens are bf16, single ones from 512 workgroups on (256 rows of 32
     // heads: 184 us for 197 by the recurrence); for few workgroups the recurrence starts sooner (one row
     // of 48 heads: 4.4 us for 6.5).  The two meet later than here: 12 rows of 48 heads, 576 workgroups,
     // take 16.9 us for 13.1, 30 rows 36.2 for 35.6.
     const int64_t tiles = (s->dv + 127) / 128;
-    if (xb == 4 || (s->T == 1 && heads * tiles < kWideBlocks)) return plan_recurrent(s, xb, sb);
-    return {LA_KERNEL_FEW, laimpl::pick_few(sb, s->dk, s->T, need.out, !need.verify), tiles, heads * tiles, 128, 256,
+    if (xb == 4 || (s->T == 1 && sat_mul(heads, tiles) < kWideBlocks)) return plan_recurrent(s, xb, sb);
+    return {LA_KERNEL_FEW, laimpl::pick_few(sb, s->dk, s->T, need.out, !need.verify), tiles, sat_mul(heads, tiles), 128, 256,
             past_caches(sat_mul(heads, (int64_t)s->dk * s->dv * sb))};
 }
 
@@ -409,7 +410,7 @@ int linattn_describe(int call, const la_shape_t *s, la_launch_info_t *info) {
     if (need.packed && in_chunks(s)) {
         const Cut c = cut_prompts(s, xb, sb);
         info->kernel = xb == 4 ? LA_KERNEL_CHUNKED_F32 : LA_KERNEL_CHUNKED;
-        info->workgroups = c.segments * s->v_heads * c.tiles;
+        info->workgroups = sat_mul(c.segments, s->v_heads * c.tiles);
         info->threads = c.plan.threads;
         info->state_cols = c.plan.cols;
         info->workspace_bytes = c.ws_bytes;
