@@ -12,7 +12,9 @@
 // accumulators of the state's update hold, lane by lane, what the product with q takes as its
 // operand (the sum over dk may run in any order, and q is read in the state's), so the state
 // never passes through LDS.  32-bit factors enter the products as sums of bf16 parts: two for
-// the state, the decayed products and (bf16 states) the decayed values, three for the decayed
+// the state, the decayed products and (bf16 states) the decayed values, which leave 2^-17 of a
+// factor where bf16 outputs or a bf16 state depend on it (2^-9 of theirs is rounded off; one output
+// in a thousand ends on the neighbour of a 32-bit computation's), three (2^-24) for the decayed
 // values that build an fp32 state.  q.k of a chunk is shared: each wavefront makes its part of
 // the ten 16 x 16 tiles on and below the diagonal and leaves it in LDS in two parts.  k and v
 // are stored as they come and read transposed where a product needs their tokens in a lane; rows
