@@ -415,6 +415,9 @@ def prepared(kind, args, kwargs):
 def linear_attn_describe(call, *args, **kwargs) -> "_linattn.LaLaunchInfo":
     """How a call with these arguments is launched (host only; raises what the call raises).
     call: "prefill", "update", "verify" or "commit", with the arguments of that entry point."""
+    if call == "prefill" and kwargs.get("workspace") is None:   # none is made for the asking
+        cu = args[6] if len(args) > 6 else kwargs["cu_seqlens"]
+        kwargs["workspace"] = cu.new_empty(0)
     lib, _dev, _fn, cargs, _keep = PREPARE["linear_attn_" + call](*args, **kwargs)
     info = _linattn.LaLaunchInfo()
     code = ("prefill", "update", "verify", "commit").index(call)

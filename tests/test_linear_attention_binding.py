@@ -34,6 +34,22 @@ def test_max_len_past_32_bits(m, max_len):
     m._attn_args("prefill", *args, cu_seqlens=cu, max_len=2 ** 31 - 1)
 
 
+def test_describe_makes_no_workspace(m, monkeypatch):
+    args, cu = _prompt(3000)
+    made = []
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: made.append(a) or empty(*a, **kw))
+    for call in (lambda: m.linear_attn_describe("prefill", *args, cu, max_len=3000),
+                 lambda: m.linear_attn_describe("prefill", *args, cu_seqlens=cu, max_len=3000)):
+        info = call()
+        assert info.launches == 3 and info.workspace_bytes > 0 and not made
+    few = [t if t is None or t.dim() > 3 else t[None, :5] for t in args]
+    assert m.linear_attn_describe("update", *few).launches == 1
+    assert m.linear_attn_describe("commit", *few[1:5]).launches == 1
+    with pytest.raises(KeyError):
+        m.linear_attn_describe("forward", *few)
+
+
 def _spread(size, device="cpu"):
     """Tensors of `size` bytes by their count, over fewer or over others' between them."""
     byte = torch.zeros(1, dtype=torch.uint8, device=device)
