@@ -13,7 +13,7 @@
 // of the rows meet once, in LDS.  bf16 parts of 32-bit factors are as for prompts.
 //
 // Measured: one token for 256 rows x 32 heads of 128 x 128 (fp32 state, a tenth of the rows padded)
-// 166 us, 6.0 TB/s; eight for 128 rows x 48 heads, verify and commit, 185 us, 6.2 TB/s.  States
+// 166 us, 6.0 TB/s; eight for 128 rows x 48 heads, verify and commit, 184-186 us, 6.2 TB/s.  States
 // past the Infinity Cache's reach go past it (184 and 209 us through it).
 #include <type_traits>
 
