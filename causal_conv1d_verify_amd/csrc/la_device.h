@@ -109,7 +109,29 @@ __device__ __forceinline__ int shared_block(int b, int set, int blocks) {
     return b / round * round + b % 8 * set + b / 8 % set;
 }
 
-// One row of a batch: its token count (-1: skip the row), its slot and its first elements.
+// A row's token count (-1: skip the row), its slot, and where its tokens are: of packed rows from
+// token `first` of them all on (seq 0), else those of sequence `seq`.
+struct Span {
+    int n;
+    int64_t slot, first, seq;
+};
+template <typename Args>
+__device__ __forceinline__ Span span_of(const Args &a, int i) {
+    Span r{a.T, a.slot_idx ? a.slot_idx[i] : i, 0, i};
+    if (a.cu_seqlens) {
+        r.first = a.cu_seqlens[i];
+        const int64_t n = (int64_t)a.cu_seqlens[i + 1] - r.first;
+        r.n = n >= 0 && n <= a.T ? (int)n : -1;
+        r.seq = 0;
+    } else if (a.num_tokens) {
+        const int n = a.num_tokens[i];
+        r.n = n >= 0 && n <= a.T ? n : -1;
+    }
+    if (r.slot < 0 || r.slot >= a.n_slots) r.n = -1;
+    return r;
+}
+
+// One row of a batch of the recurrence: its token count, its slot and its first elements.
 struct Row {
     int n;
     int64_t slot, q, k, v, o, g;
@@ -118,26 +140,10 @@ __device__ __forceinline__ Row uniform(const Row &r) {
     return Row{uniform(r.n), uniform(r.slot), uniform(r.q), uniform(r.k), uniform(r.v), uniform(r.o), uniform(r.g)};
 }
 __device__ __forceinline__ Row row_of(const AttnArgs &a, int i) {
-    Row r;
-    r.slot = a.slot_idx ? a.slot_idx[i] : i;
-    int64_t first = 0, seq = i;
-    r.n = a.T;
-    if (a.cu_seqlens) {
-        first = a.cu_seqlens[i];
-        const int64_t n = (int64_t)a.cu_seqlens[i + 1] - first;
-        r.n = n >= 0 && n <= a.T ? (int)n : -1;
-        seq = 0;
-    } else if (a.num_tokens) {
-        const int n = a.num_tokens[i];
-        r.n = n >= 0 && n <= a.T ? n : -1;
-    }
-    if (r.slot < 0 || r.slot >= a.n_slots) r.n = -1;
-    r.q = seq * a.q_seq + first * a.q_tok;
-    r.k = seq * a.k_seq + first * a.k_tok;
-    r.v = seq * a.v_seq + first * a.v_tok;
-    r.o = seq * a.o_seq + first * a.o_tok;
-    r.g = seq * a.g_seq + first * a.g_tok;
-    return r;
+    const Span s = span_of(a, i);
+    return Row{s.n, s.slot, s.seq * a.q_seq + s.first * a.q_tok, s.seq * a.k_seq + s.first * a.k_tok,
+               s.seq * a.v_seq + s.first * a.v_tok, s.seq * a.o_seq + s.first * a.o_tok,
+               s.seq * a.g_seq + s.first * a.g_tok};
 }
 
 __device__ __forceinline__ float load_one(const float *p) { return *p; }
@@ -147,20 +153,42 @@ __device__ __forceinline__ void store_one(Bf16 *p, float x) {
     p->bits = __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
+// 1 / sqrt(sum / dim + eps) of the sum of squares that `total(scale)` gives for values times
+// `scale`.  A sum that leaves fp32's range is taken again over values scaled by a power of two
+// (the same for everyone who shares the sum).  The result times a value stays accurate: it is
+// returned as a pair (mult, pre) to be applied as (value * pre) * mult.
+template <typename F>
+__device__ __forceinline__ void inverse_rms(F total, int dim, float eps, float &mult, float &pre) {
+    pre = 1.0f;
+    float sum = total(1.0f);
+    float e = eps;
+    if (__builtin_expect(!(sum < INFINITY), 0)) {                 // overflow (or not finite)
+        pre = 0x1p-80f;
+        sum = total(pre);
+        e = (eps * pre) * pre;
+    } else if (__builtin_expect(sum < 0x1p-100f && eps < 0x1p-100f, 0)) {
+        pre = 0x1p80f;
+        sum = total(pre);
+        e = (eps * pre) * pre;
+    }
+    mult = 1.0f / sqrtf(sum / (float)dim + e);
+}
+
 // Segment `id` of the rows in order, each row cut into ceil(tokens / seg_len) of them and one
 // where it has no tokens; row -1 where there are fewer.  Rows that are skipped have none, nor
 // has a row that would end past a.segments or a.places (more tokens than the caller declared).
 // `place` is the row's first place in the workspace, where rows of one segment have none.  Called
 // by a whole workgroup of W wavefronts, `shared` is three words of LDS.
 struct Segment { int row, index; bool last; int place; };
-__device__ __forceinline__ int segments_of(const AttnArgs &a, int i) {
-    const Row r = row_of(a, i);
-    return r.n < 0 ? 0 : r.n == 0 ? 1 : (int)(((uint32_t)r.n + (uint32_t)a.seg_len - 1) / (uint32_t)a.seg_len);
+template <typename Args>
+__device__ __forceinline__ int segments_of(const Args &a, int i) {
+    const int n = span_of(a, i).n;
+    return n < 0 ? 0 : n == 0 ? 1 : (int)(((uint32_t)n + (uint32_t)a.seg_len - 1) / (uint32_t)a.seg_len);
 }
 __device__ __forceinline__ int places_of(int segments) { return segments > 1 ? segments : 0; }
-template <int W>
-__device__ __forceinline__ Segment find_segment(const AttnArgs &a, int id, int64_t *shared) {
-    if (a.seg_len >= a.T) return row_of(a, id).n < 0 ? Segment{-1, 0, true, 0} : Segment{id, 0, true, 0};
+template <int W, typename Args>
+__device__ __forceinline__ Segment find_segment(const Args &a, int id, int64_t *shared) {
+    if (a.seg_len >= a.T) return span_of(a, id).n < 0 ? Segment{-1, 0, true, 0} : Segment{id, 0, true, 0};
     __shared__ int sums[2][W];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int64_t before = 0, places = 0;                // of the rows before these
@@ -192,8 +220,8 @@ __device__ __forceinline__ Segment find_segment(const AttnArgs &a, int id, int64
 }
 
 // The first place of row i in the workspace (i the same for the workgroup).
-template <int W>
-__device__ __forceinline__ int64_t first_place(const AttnArgs &a, int i) {
+template <int W, typename Args>
+__device__ __forceinline__ int64_t first_place(const Args &a, int i) {
     __shared__ int64_t sums[W];
     int64_t own = 0;
     for (int r = threadIdx.x; r < i; r += 64 * W) own += places_of(segments_of(a, r));

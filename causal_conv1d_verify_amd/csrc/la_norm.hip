@@ -18,27 +18,6 @@ __device__ __forceinline__ float sigmoid(float z) {
     return z < 0.0f ? e * r : r;
 }
 
-// 1 / sqrt(sum / dim + eps) of the sum of squares that `total(scale)` gives for values times
-// `scale`.  A sum that leaves fp32's range is taken again over values scaled by a power of two
-// (the same for everyone who shares the sum).  The result times a value stays accurate: it is
-// returned as a pair (mult, pre) to be applied as (value * pre) * mult.
-template <typename F>
-__device__ __forceinline__ void inverse_rms(F total, int dim, float eps, float &mult, float &pre) {
-    pre = 1.0f;
-    float sum = total(1.0f);
-    float e = eps;
-    if (__builtin_expect(!(sum < INFINITY), 0)) {                 // overflow (or not finite)
-        pre = 0x1p-80f;
-        sum = total(pre);
-        e = (eps * pre) * pre;
-    } else if (__builtin_expect(sum < 0x1p-100f && eps < 0x1p-100f, 0)) {
-        pre = 0x1p80f;
-        sum = total(pre);
-        e = (eps * pre) * pre;
-    }
-    mult = 1.0f / sqrtf(sum / (float)dim + e);
-}
-
 // A group (one head of one row) lies across LG lanes, each holding E vectors of 8 channels,
 // vector e of lane l at channel 8 * (l + LG * e); 256 / LG groups per workgroup.
 template <typename XT, int LG, int E>
