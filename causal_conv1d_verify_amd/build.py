@@ -1,5 +1,5 @@
-"""Builds libconvverify.so and liblinattn.so (HIP kernels for gfx950 + their C ABIs) and the call
-module _lacall.so in-tree with hipcc.
+"""Builds libconvverify.so, liblinattn.so and libseqops.so (HIP kernels for gfx950 + their C ABIs) and
+the call modules _lacall.so and _sqcall.so in-tree with hipcc.
 
 Usage: python -m causal_conv1d_verify_amd.build   (or __graft_entry__.build())
 """
@@ -24,6 +24,13 @@ LIB_WC = os.path.join(PKG, "libconvverify_wc.so")
 LIB_LA = os.path.join(PKG, "liblinattn.so")
 # torch tensors to liblinattn.so in C (linear_attention.py has the same in Python).
 LIB_CALL = os.path.join(PKG, "_lacall.so")
+
+
+def _beside(lib, name):
+    """Of the selective scan, rotated heads and the verdict on drafts: libseqops.so beside
+    liblinattn.so, and its call module _sqcall.so beside the other one."""
+    return os.path.join(os.path.dirname(lib), name)
+
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -59,10 +66,14 @@ SOURCES_LA = [
     (f"la_{name}.hip", f"la_{name}", [f"--offload-arch={ARCH}", *DEVICE_FLAGS])
     for name in ("chunked", "chunked_f32", "few", "recurrent", "norm")
 ] + [("la_api.cpp", "la_api", [])]
+SOURCES_SQ = [
+    (f"sq_{name}.hip", f"sq_{name}", [f"--offload-arch={ARCH}", *DEVICE_FLAGS])
+    for name in ("scan", "rotary", "accept")
+] + [("sq_api.cpp", "sq_api", [])]
 
 
 def _call_module():
-    """The compile flags and the link flags of the call module: Python's and torch's."""
+    """The compile flags and the link flags of a call module: Python's and torch's."""
     import sysconfig
 
     import torch
@@ -71,11 +82,11 @@ def _call_module():
     return ([f"-I{sysconfig.get_paths()['include']}", f"-isystem{root}/include",
              f"-isystem{root}/include/torch/csrc/api/include", "-DUSE_ROCM",
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"],
-            [f"-L{PKG}", "-llinattn", "-Wl,-rpath,$ORIGIN", f"-L{root}/lib", "-lc10", "-lc10_hip",
+            [f"-L{PKG}", "-Wl,-rpath,$ORIGIN", f"-L{root}/lib", "-lc10", "-lc10_hip",
              "-ltorch_cpu", "-ltorch_python"])
 
 
-MAX_JOBS = max(1, min(len(SOURCES) + len(SOURCES_WC) + len(SOURCES_LA), int(os.environ.get("MAX_JOBS", os.cpu_count() or 4))))
+MAX_JOBS = max(1, min(len(SOURCES) + len(SOURCES_WC) + len(SOURCES_LA) + len(SOURCES_SQ), int(os.environ.get("MAX_JOBS", os.cpu_count() or 4))))
 
 
 def _run(cmd):
@@ -87,34 +98,40 @@ def _run(cmd):
 
 
 def build(verbose: bool = True) -> str:
-    """Builds libconvverify.so, the write-count test library libconvverify_wc.so, liblinattn.so
-    and _lacall.so.  Only the last needs Python's and torch's headers: where it cannot be built the
-    libraries are there all the same, and the error is raised behind them."""
+    """Builds libconvverify.so, the write-count test library libconvverify_wc.so, liblinattn.so,
+    libseqops.so and the call modules.  Only the last need Python's and torch's headers: where one
+    cannot be built the libraries are there all the same, and the error is raised behind them."""
     os.makedirs(os.path.join(BUILD, "wc"), exist_ok=True)
     t0 = time.time()
     pending = []
     libs = []
-    for sources, lib in ((SOURCES, LIB), (SOURCES_WC, LIB_WC), (SOURCES_LA, LIB_LA)):
+    for sources, lib in ((SOURCES, LIB), (SOURCES_WC, LIB_WC), (SOURCES_LA, LIB_LA),
+                         (SOURCES_SQ, _beside(LIB_LA, "libseqops.so"))):
         objs = []
         for src, stem, extra in sources:
             obj = os.path.join(BUILD, stem + ".o")
             pending.append([HIPCC, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
             objs.append(obj)
         libs.append((lib, objs))
-    call_obj, call_cmd, call_error = os.path.join(BUILD, "la_call.o"), None, None
+    calls = []                                     # (module, its object, its library)
+    for stem, lib, module in (("la_call", "-llinattn", LIB_CALL),
+                              ("sq_call", "-lseqops", _beside(LIB_CALL, "_sqcall.so"))):
+        calls.append((module, os.path.join(BUILD, stem + ".o"), lib))
+    errors = {}                                    # of a module
     try:
         compile_call, link_call = _call_module()
-        call_cmd = [HIPCC, *COMMON, *compile_call, "-c", os.path.join(CSRC, "la_call.cpp"), "-o", call_obj]
-        pending.insert(0, call_cmd)
+        for _, obj, _ in calls:
+            src = os.path.basename(obj)[:-2] + ".cpp"
+            pending.insert(0, [HIPCC, *COMMON, *compile_call, "-c", os.path.join(CSRC, src), "-o", obj])
     except Exception as e:
-        call_error = e
+        errors = {module: e for module, _, _ in calls}
     running = []
 
     def reap(cmd, p):
-        nonlocal call_error
         out, err = p.communicate()
-        if p.returncode != 0 and cmd is call_cmd:
-            call_error = RuntimeError(f"build step failed ({p.returncode}):\n{' '.join(cmd)}\n{out}\n{err}")
+        module = {obj: m for m, obj, _ in calls}.get(cmd[-1])
+        if p.returncode != 0 and module:
+            errors[module] = RuntimeError(f"build step failed ({p.returncode}):\n{' '.join(cmd)}\n{out}\n{err}")
             return
         if p.returncode != 0:
             for _, q in running:
@@ -140,16 +157,20 @@ def build(verbose: bool = True) -> str:
 
     for lib, objs in libs:
         link(lib, objs)
-    try:
-        if call_error is not None:
-            raise call_error
-        link(LIB_CALL, [call_obj], link_call)
-    except Exception:
-        if os.path.exists(LIB_CALL):               # an older one's view of the library may be another
-            os.remove(LIB_CALL)
-        raise
+    for module, obj, lib in calls:
+        try:
+            if module in errors:
+                raise errors[module]
+            link(module, [obj], (*link_call[:1], lib, *link_call[1:]))
+        except Exception as e:
+            errors[module] = e
+            if os.path.exists(module):             # an older one's view of the library may be another
+                os.remove(module)
+    if errors:
+        raise next(iter(errors.values()))
     if verbose:
-        print(f"built {LIB}, {LIB_WC}, {LIB_LA} and {LIB_CALL} in {time.time() - t0:.1f}s", file=sys.stderr)
+        print(f"built {', '.join(lib for lib, _ in libs)} and {', '.join(c[0] for c in calls)} in "
+              f"{time.time() - t0:.1f}s", file=sys.stderr)
     return LIB
 
 
