@@ -16,23 +16,15 @@ namespace {
 
 using namespace laimpl;
 
-struct Verdict {
-    int num, last;                // num 0: the row is skipped
-    int against;                  // 1: the weights are what the draft leaves of the target
-    int removed;                  // tokens tried without a draft, which weigh nothing
-    uint64_t way;                 // the accepted tokens' places
-    int token[32];
-};
-
 __device__ __forceinline__ double lane_value(double v, int lane) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// Row i's verdict, by one wavefront.
+// Row i's verdict, by one wavefront; `tell`: it goes to the outputs and to the workspace too.
 template <typename PT>
-__device__ __forceinline__ void judge(const AcceptArgs &a, int i, Verdict *v) {
+__device__ __forceinline__ void judge(const AcceptArgs &a, int i, bool tell, Verdict *v) {
     const int t = threadIdx.x & 63;
     const bool in = t < a.T;
     const int token = in ? a.tokens[i * a.tokens_row + t] : -1;
@@ -46,7 +38,7 @@ __device__ __forceinline__ void judge(const AcceptArgs &a, int i, Verdict *v) {
         if (a.draft) q = load_one(static_cast<const PT *>(a.draft) + i * a.draft_seq + parent * a.draft_tok + token);
         u = a.uniform[i * a.uniform_row + t - 1];
     }
-    int last = 0, removed = 0;
+    int last = 0;
     uint64_t way = 1, gone = 0;
     bool against = false;
     if (!a.parent) {
@@ -80,14 +72,22 @@ __device__ __forceinline__ void judge(const AcceptArgs &a, int i, Verdict *v) {
             }
         }
     }
-    removed = __builtin_popcountll(gone);
-    if (gone >> t & 1) v->token[__builtin_popcountll(gone & ((1ull << t) - 1))] = token;
+    const int num = skip ? 0 : __builtin_popcountll(way), removed = __builtin_popcountll(gone);
+    auto put = [&](Verdict *to) {
+        if (gone >> t & 1) to->token[__builtin_popcountll(gone & ((1ull << t) - 1))] = token;
+        if (t == 0) to->num = num, to->last = last, to->against = against, to->removed = removed;
+    };
+    put(v);
+    if (!tell) return;
+    put(a.verdicts + i);
+    if (skip) return;
+    if (a.path && in) {
+        if (way >> t & 1) a.path[i * a.path_row + __builtin_popcountll(way & ((1ull << t) - 1))] = t;
+        if (t >= num) a.path[i * a.path_row + t] = -1;
+    }
     if (t == 0) {
-        v->num = skip ? 0 : __builtin_popcountll(way);
-        v->last = last;
-        v->against = against;
-        v->removed = removed;
-        v->way = way;
+        a.num[i] = num;
+        if (a.last) a.last[i] = last;
     }
 }
 
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(256) void sums(const AcceptArgs a) {
     __shared__ Verdict v;
     const int chunk = blockIdx.x % a.chunks, i = blockIdx.x / a.chunks;
     const int wave = uniform((int)(threadIdx.x >> 6));
-    if (wave == 0) judge<PT>(a, i, &v);
+    if (wave == 0) judge<PT>(a, i, chunk == 0, &v);
     __syncthreads();
     if (v.num == 0) return;                        // same for the workgroup
     const Weights<PT> weights(a, i, v);
@@ -216,38 +216,43 @@ __device__ __forceinline__ double before_lane(double own, double *waves, double 
     return base + (lane ? y : 0.0);
 }
 
+// Of the workgroup's lanes in order, the value of the first that has one, and that of the last that
+// has another; -1 where none has.
+struct Ends { int first, last; };
+__device__ __forceinline__ Ends ends_of(bool first, int value, bool last, int other, int (*slots)[4]) {
+    const int wave = threadIdx.x >> 6;
+    const uint64_t f = __builtin_amdgcn_ballot_w64(first), l = __builtin_amdgcn_ballot_w64(last);
+    const int from = __builtin_amdgcn_readlane(value, f ? __builtin_ctzll(f) : 0);
+    const int to = __builtin_amdgcn_readlane(other, l ? 63 - __builtin_clzll(l) : 0);
+    if ((threadIdx.x & 63) == 0) slots[0][wave] = f ? from : -1, slots[1][wave] = l ? to : -1;
+    __syncthreads();
+    Ends e{-1, -1};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (e.first < 0) e.first = slots[0][w];
+        if (slots[1][w] >= 0) e.last = slots[1][w];
+    }
+    return e;
+}
+
 template <typename PT>
 __global__ __launch_bounds__(256) void pick(const AcceptArgs a) {
     __shared__ Verdict v;
-    __shared__ double waves[4];
-    __shared__ double start;
-    __shared__ int found, final;
+    __shared__ double waves[4], start;
+    __shared__ int slots[2][2][4];
     const int i = blockIdx.x, tid = threadIdx.x, wave = uniform(tid >> 6);
-    if (wave == 0) judge<PT>(a, i, &v);
-    __syncthreads();
-    if (v.num == 0) return;                        // same for the workgroup
-    if (tid < a.T) {
-        if (a.path) {
-            if (v.way >> tid & 1) a.path[i * a.path_row + __builtin_popcountll(v.way & ((1ull << tid) - 1))] = tid;
-            if (tid >= v.num) a.path[i * a.path_row + tid] = -1;
-        }
-        if (tid == 0) {
-            a.num[i] = v.num;
-            if (a.last) a.last[i] = v.last;
-        }
-    }
-    Weights<PT> weights(a, i, v);
     double *sums = a.sums + (int64_t)i * a.parts;
-    const double share = a.uniform[i * a.uniform_row + a.T - 1];
     const int per = (a.parts + 255) / 256;
     const int first = tid * per < a.parts ? tid * per : a.parts, last = first + per < a.parts ? first + per : a.parts;
-
-    double own, base, all;
-    for (bool again = false;; again = true) {
-        own = 0.0;
-        for (int k = first; k < last; ++k) own += sums[k];
-        base = before_lane(own, waves, all);
-        if (all > 0.0 || again || (!weights.q && !weights.removed)) break;
+    double own = 0.0, base, all;
+    for (int k = first; k < last; ++k) own += sums[k];
+    const double share = a.uniform[i * a.uniform_row + a.T - 1];
+    if (tid < (int)(sizeof(Verdict) / 4)) reinterpret_cast<int *>(&v)[tid] = reinterpret_cast<const int *>(a.verdicts + i)[tid];
+    __syncthreads();
+    if (v.num == 0) return;                        // same for the workgroup
+    Weights<PT> weights(a, i, v);
+    base = before_lane(own, waves, all);
+    if (!(all > 0.0) && (weights.q || weights.removed)) {
         // nothing is left beside the tokens tried: the target's own probabilities
         weights.q = nullptr;
         weights.removed = 0;
@@ -256,6 +261,9 @@ __global__ __launch_bounds__(256) void pick(const AcceptArgs a) {
             if ((tid & 63) == 0) sums[k] = s;
         }
         __syncthreads();                           // (the row's sums are this workgroup's alone)
+        own = 0.0;
+        for (int k = first; k < last; ++k) own += sums[k];
+        base = before_lane(own, waves, all);
     }
     if (!(all > 0.0)) {
         if (tid == 0) a.next[i] = -1;
@@ -264,31 +272,22 @@ __global__ __launch_bounds__(256) void pick(const AcceptArgs a) {
     const double passed = share * all;
 
     // ---- the part
-    if (tid == 0) found = a.parts, final = -1;
-    __syncthreads();
+    int over = -1, some = -1;
     double at = base;
-    for (int k = first; k < last; ++k) {
+    for (int k = first; k < last && over < 0; ++k) {
         const double s = sums[k];
-        if (s > 0.0) atomicMax(&final, k);
-        if (at + s > passed) {
-            atomicMin(&found, k);
-            break;
-        }
-        at += s;
+        if (s > 0.0) some = k;
+        if (at + s > passed) over = k;
+        else at += s;
     }
-    __syncthreads();
-    const bool none = found == a.parts;            // rounding: the last weight that there is
-    const int part = none ? final : found;
+    const Ends parts = ends_of(over >= 0, over, some >= 0, some, slots[0]);
+    const bool none = parts.first < 0;             // rounding: the last weight that there is
+    const int part = none ? parts.last : parts.first;
     if (part >= first && part < last) {
         double s = base;
         for (int k = first; k < part; ++k) s += sums[k];
         start = s;
     }
-    __syncthreads();
-    const double from = start;
-    __syncthreads();
-    if (tid == 0) found = 4 * 256, final = -1;
-    __syncthreads();
 
     // ---- the weight
     const int begin = part * kPart;
@@ -296,19 +295,19 @@ __global__ __launch_bounds__(256) void pick(const AcceptArgs a) {
     weights.of(weights.load(begin + 4 * tid), w);
     if (weights.any_removed(begin, begin + kPart)) weights.take_removed(begin + 4 * tid, w);
     double whole;
-    at = from + before_lane((w[0] + w[1]) + (w[2] + w[3]), waves, whole);
-    bool over = false;
+    at = before_lane((w[0] + w[1]) + (w[2] + w[3]), waves, whole);
+    at += start;                                   // written before the barriers of the sums
+    over = some = -1;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         at += w[e];
-        if (w[e] > 0.0) atomicMax(&final, 4 * tid + e);
-        if (!none && !over && at > passed && w[e] > 0.0) {
-            atomicMin(&found, 4 * tid + e);
-            over = true;
+        if (w[e] > 0.0) {
+            some = 4 * tid + e;
+            if (!none && over < 0 && at > passed) over = 4 * tid + e;
         }
     }
-    __syncthreads();
-    if (tid == 0) a.next[i] = begin + (found < 4 * 256 ? found : final);
+    const Ends which = ends_of(over >= 0, over, some >= 0, some, slots[1]);
+    if (tid == 0) a.next[i] = begin + (which.first >= 0 ? which.first : which.last);
 }
 
 }  // namespace

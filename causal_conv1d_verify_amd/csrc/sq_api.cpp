@@ -204,7 +204,9 @@ int check_accept(const sq_accept_shape_t *s, bool parent, bool draft, bool path,
 }
 
 int64_t accept_parts(const sq_accept_shape_t *s) { return (s->vocab + sqimpl::kPart - 1) / sqimpl::kPart; }
-int64_t accept_bytes(const sq_accept_shape_t *s) { return (s->n_seq * accept_parts(s) * 8 + 15) / 16 * 16; }
+int64_t accept_bytes(const sq_accept_shape_t *s) {
+    return (s->n_seq * (accept_parts(s) * 8 + (int64_t)sizeof(sqimpl::Verdict)) + 15) / 16 * 16;
+}
 
 }  // namespace
 
@@ -358,7 +360,8 @@ int accept_drafts(const sq_accept_shape_t *s, const int32_t *tokens, const int32
     a.path_row = s->path_stride;
     a.target_seq = s->target_seq_stride; a.target_tok = s->target_tok_stride;
     a.draft_seq = s->draft_seq_stride; a.draft_tok = s->draft_tok_stride;
-    a.sums = static_cast<double *>(workspace);
+    a.verdicts = static_cast<sqimpl::Verdict *>(workspace);
+    a.sums = reinterpret_cast<double *>(a.verdicts + s->n_seq);
     a.n_seq = s->n_seq; a.T = s->T; a.vocab = s->vocab;
     a.parts = (int32_t)accept_parts(s);
     a.chunks = (a.parts + p.parts - 1) / p.parts;

@@ -57,6 +57,13 @@ struct RotaryPlan {
 };
 RotaryPlan pick_rotary(int x_bytes, int dim);
 
+// What is known of a row before its next token is drawn.
+struct Verdict {
+    int32_t num, last;                  // num 0: the row is skipped
+    int32_t against;                    // 1: the weights are what the draft leaves of the target
+    int32_t removed;                    // tokens tried without a draft, which weigh nothing
+    int32_t token[32];                  // they
+};
 struct AcceptArgs {
     const int32_t *tokens, *parent;
     const void *target, *draft;
@@ -64,6 +71,7 @@ struct AcceptArgs {
     const int32_t *slot_idx;
     int32_t *num, *next, *last, *path;
     int64_t tokens_row, parent_row, uniform_row, path_row, target_seq, target_tok, draft_seq, draft_tok;
+    Verdict *verdicts;                  // [n_seq]
     double *sums;                       // [n_seq, parts]: of kPart consecutive weights each
     int32_t n_seq, T, vocab, parts, chunks;
 };
