@@ -68,7 +68,7 @@ SOURCES_LA = [
 ] + [("la_api.cpp", "la_api", [])]
 SOURCES_SQ = [
     (f"sq_{name}.hip", f"sq_{name}", [f"--offload-arch={ARCH}", *DEVICE_FLAGS])
-    for name in ("scan", "rotary", "accept")
+    for name in ("prompt", "scan", "rotary", "accept")
 ] + [("sq_api.cpp", "sq_api", [])]
 
 

@@ -66,6 +66,12 @@ int check_scan(const sq_scan_shape_t *s, const Need &need, int *xb, int *sb, boo
         Dim d[2] = {{toks, s->out_tok_stride}, {rows ? s->n_seq : 1, s->out_seq_stride}};
         if (!apart(s->d, d, 2)) return fail(CV_EINVAL, "the strides of out make its rows overlap");
     }
+    if (need.packed)
+        for (const Stride &d : {Stride{"x_tok_stride", s->x_tok_stride, true, 0}, {"dt_tok_stride", s->dt_tok_stride, true, 0},
+                                {"z_tok_stride", s->z_tok_stride, true, 0}, {"b_tok_stride", s->b_tok_stride, true, 0},
+                                {"out_tok_stride", s->out_tok_stride, true, 0}})
+            if (sat_add(sat_mul(3, d.stride), s->d) > INT32_MAX / *xb)
+                return fail(CV_ENOTSUP, "%s (%lld): four tokens span more than 2 GiB", d.name, (long long)d.stride);
     *empty = s->n_seq == 0;
     return CV_OK;
 }
@@ -106,7 +112,7 @@ sqimpl::ScanArgs scan_args(const sq_scan_shape_t *s, const sq_scan_data_t *p, co
 // slots would have; then rows are cut into segments of about that share, at the price of passing
 // over all but the last of them twice.
 struct Cut {
-    sqimpl::ScanPlan plan;
+    sqimpl::PromptPlan plan;
     int64_t tiles, segments, places, ws_bytes;
     int32_t seg_len;
 };
@@ -114,7 +120,7 @@ Cut cut_prompts(const sq_scan_shape_t *s, int xb, int sb) {
     constexpr int64_t kSlots = 512;
     constexpr int64_t kLeast = 4;                  // stages
     Cut c{};
-    c.plan = sqimpl::pick_scan(xb, sb, s->d_state, true);
+    c.plan = sqimpl::pick_prompt(xb, sb, s->d_state);
     const int64_t stage = c.plan.stage;
     c.tiles = (s->d + c.plan.channels - 1) / c.plan.channels;
     c.segments = s->n_seq;

@@ -29,15 +29,22 @@ struct ScanArgs {
     float *ws_total;              // each channel's sum of delta over each
 };
 
-// run makes the outputs and the last state (out false: the state only); where rows are cut, first
-// leaves what each segment adds to a state of zeros, and the row's first state, in the workspace,
-// and combine makes the state behind each segment of them.
+// Up to 32 tokens of each row (out false: the state only).
 struct ScanPlan {
-    const void *run, *first, *combine;
-    int channels, threads, stage;       // channels per workgroup; tokens of a stage
-    int64_t ws_floats, total_floats;    // of one workgroup's state, and of its sums of delta
+    const void *run;
+    int channels, threads;              // of a workgroup
 };
 ScanPlan pick_scan(int x_bytes, int state_bytes, int d_state, bool out);
+
+// Packed prompts.  run makes the outputs and the last state; where rows are cut, first leaves what
+// each segment adds to a state of zeros, and the row's first state, in the workspace, and combine
+// makes the state behind each segment of them.
+struct PromptPlan {
+    const void *run, *first, *combine;
+    int channels, threads, stage;       // of a workgroup; tokens of a stage
+    int64_t ws_floats, total_floats;    // of one workgroup's state, and of its sums of delta
+};
+PromptPlan pick_prompt(int x_bytes, int state_bytes, int d_state);
 
 struct RotaryArgs {
     const void *x[2], *weight[2];       // q, k

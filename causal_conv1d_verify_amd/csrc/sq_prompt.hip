@@ -1,0 +1,295 @@
+// The selective scan of packed prompts: for each channel c and state n
+//
+//   h <- exp(delta A[c,n]) h + (delta x) B[n],   y = sum_n C[n] h + D x,   out = y silu(z)
+//
+// The decay is another one for every channel and state, so no product of matrices makes it: each
+// state update is a multiply, an exponential and two multiply-adds on the vector units (24 cycles of
+// a wavefront in all: 4 + 8 + 4 + 4, and 1.5 of the sum across lanes), which bound this kernel.  What can be taken off them is:
+// the products (delta x) B are a rank-one product for each token, four tokens of 16 states x 16
+// channels in one matrix instruction beside them.
+//
+// A wavefront has 16 channels from a segment's first token to its last, lane l channel l % 16 and, of
+// every 16 states, the four from 4 (l / 16) on; tokens go in groups of four, of which lane l loads x, dt
+// and z of token l / 16 and makes its delta and gate.  The deltas of a group come back through LDS in
+// one vector, as C does (a stage of 16 tokens, converted once).  The four lanes' sums of four tokens
+// are added and dealt out in three lane swaps, to the lane that has the token.  Loads are a stage
+// ahead.  No barrier: wavefronts are alone.
+#include "sq_scan_device.h"
+
+namespace sqimpl {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// p[i] of lanes 16 g + j for the four g added up, token i's on the lanes of g = i.
+__device__ __forceinline__ float deal_sums(const float (&p)[4]) {
+    auto swap32 = [](float a, float b) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    };
+    const float even = swap32(p[0], p[2]), odd = swap32(p[1], p[3]);   // tokens 0 | 2, 1 | 3
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(even), __float_as_uint(odd), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The elements of a segment's tokens that a wavefront loads or stores in groups of four tokens, each
+// through a buffer resource that ends with the segment's last token: loads past it are 0, and stores
+// are dropped, as at the offset kNowhere.
+constexpr uint32_t kNowhere = 0x80000000u;
+template <typename XT>
+struct Tokens {
+    const XT *p;
+    uint32_t tok, width;          // of a token; four tokens lie within 2 GiB
+    __device__ __forceinline__ uint32_t offset(int token, int element) const {
+        return (token * tok + element) * (uint32_t)sizeof(XT);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t from(int s4, int n) const {
+        const int left = n - s4 < 4 ? n - s4 : 4;
+        const uint32_t bytes = ((left - 1) * tok + width) * (uint32_t)sizeof(XT);
+        return cvimpl::make_rsrc(p + (int64_t)s4 * tok, left > 0 ? bytes : 0u);
+    }
+};
+template <typename XT>
+__device__ __forceinline__ XT load_from(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
+    if constexpr (sizeof(XT) == 2) return __builtin_bit_cast(XT, __builtin_amdgcn_raw_buffer_load_b16(r, (int)offset, 0, 0));
+    else return __builtin_bit_cast(XT, __builtin_amdgcn_raw_buffer_load_b32(r, (int)offset, 0, 0));
+}
+template <typename XT>
+__device__ __forceinline__ void store_to(__amdgpu_buffer_rsrc_t r, uint32_t offset, float y) {
+    XT v;
+    store_one(&v, y);
+    if constexpr (sizeof(XT) == 2) __builtin_amdgcn_raw_buffer_store_b16(v.bits, r, (int)offset, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, (int)offset, 0, 0);
+}
+
+// NT: sixteens of states.  OUT: the outputs and the last state; else what each segment of a cut row
+// adds to a state of zeros, and the row's first state, to the workspace.
+template <typename XT, typename ST, int NT, bool OUT>
+__global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
+    constexpr int NP = 16 * NT, NL = 4 * NT;
+    __shared__ alignas(16) float deltas[4][4][16][4];             // [wave][group][channel][token]
+    __shared__ alignas(16) float cs[4][OUT ? kStage : 1][OUT ? NP : 4];
+    __shared__ int64_t found[3];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int j = lane & 15, g = lane >> 4;
+    const int tile = uniform((int)(blockIdx.x % a.tiles)), id = uniform((int)(blockIdx.x / a.tiles));
+    const Segment seg = find_segment<4>(a, id, found);
+    if (seg.row < 0) return;                       // same for the workgroup
+    Span row = span_of(a, seg.row);
+    row = Span{uniform(row.n), uniform(row.slot), uniform(row.first), uniform(row.seq)};
+    const bool init = !a.has_init || uniform(a.has_init[seg.row]) != 0;
+    const bool cut = !seg.last || seg.index > 0;
+    if (!OUT && !cut) return;
+    if (row.n == 0 && (init || !a.write_state)) return;
+    const int c0 = tile * kChannels + 16 * wave;
+    if (c0 >= a.d) return;                         // a whole wavefront
+    const bool own = c0 + j < a.d;
+    const int c = own ? c0 + j : a.d - 1;
+
+    // ---- the states that enter
+    ST *state = static_cast<ST *>(a.state) + row.slot * a.s_slot + (int64_t)c * a.d_state + 4 * g;
+    float h[NT][4], decay[NT][4];
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[q][r] = decay[q][r] = 0.0f;
+    auto from_pool = [&]() {
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+            if (16 * q + 4 * g < a.d_state) load_vec<4>(state + 16 * q, h[q]);
+    };
+    auto place = [&](int index) {
+        return ((int64_t)(seg.place + index) * a.tiles + tile) * 256 + tid;
+    };
+    auto from_workspace = [&](int index) {
+        const float *ws = a.ws + place(index) * NL;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) load_vec<4>(ws + 4 * q, h[q]);
+    };
+    auto to_workspace = [&]() {
+        float *ws = a.ws + place(seg.index) * NL;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) store_vec<4>(ws + 4 * q, h[q]);
+    };
+    if (!OUT) {
+        if (seg.last) {                            // the row's first state, in its last place
+            if (init) from_pool();
+            to_workspace();
+            return;
+        }
+    } else if (cut) {
+        from_workspace(seg.index > 0 ? seg.index - 1 : segments_of(a, seg.row) - 1);
+    } else if (init) {
+        from_pool();
+    }
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+        if (16 * q + 4 * g < a.d_state) {
+            load_vec<4>(a.A + (int64_t)c * a.d_state + 16 * q + 4 * g, decay[q]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) decay[q][r] *= kLog2e;
+        }
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = OUT && a.D ? a.D[c] : 0.0f;
+
+    // ---- the tokens
+    const int begin = seg.index * a.seg_len;
+    const int n = row.n - begin < a.seg_len ? row.n - begin : a.seg_len;
+    const int64_t t0 = row.first + begin;
+    auto tokens_of = [&](const void *p, int64_t seq, int64_t tok, int width) {
+        return Tokens<XT>{static_cast<const XT *>(p) + row.seq * seq + t0 * tok, (uint32_t)tok, (uint32_t)width};
+    };
+    const Tokens<XT> x = tokens_of(a.x, a.x_seq, a.x_tok, a.d), dt = tokens_of(a.dt, a.dt_seq, a.dt_tok, a.d);
+    const Tokens<XT> z = a.z ? tokens_of(a.z, a.z_seq, a.z_tok, a.d) : x, out = tokens_of(a.out, a.o_seq, a.o_tok, a.d);
+    const Tokens<XT> B = tokens_of(a.B, a.b_seq, a.b_tok, a.d_state);
+    const uint32_t off_x = own ? x.offset(g, c) : kNowhere, off_dt = own ? dt.offset(g, c) : kNowhere;
+    const uint32_t off_z = own ? z.offset(g, c) : kNowhere, off_out = own ? out.offset(g, c) : kNowhere;
+    const uint32_t off_b = B.offset(g, j);
+    const int tc = lane >> 2, n0 = (lane & 3) * NL;   // C: the token of the stage and the states that this lane brings
+    const XT *C = OUT ? static_cast<const XT *>(a.C) + row.seq * a.c_seq + t0 * a.c_tok : nullptr;
+    XT next_x[4], next_dt[4], next_z[4], next_b[4][NT];
+    Run<XT, NL> next_c;
+    // The stage from token s on.  There is no branch among its loads, which would wait for them:
+    // past the row's end x, dt, z and B are 0, and C the last token's, for outputs that nobody has.
+    auto fetch = [&](int s) {
+        if constexpr (OUT) next_c.load_near(C + (int64_t)(s + tc < n ? s + tc : n - 1) * a.c_tok, n0, a.d_state);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int s4 = s + 4 * k;
+            next_x[k] = load_from<XT>(x.from(s4, n), off_x);
+            next_dt[k] = load_from<XT>(dt.from(s4, n), off_dt);
+            if constexpr (OUT) next_z[k] = load_from<XT>(z.from(s4, n), off_z);
+            const auto b = B.from(s4, n);
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+                next_b[k][q] = load_from<XT>(b, 16 * q + j < a.d_state ? off_b + 16 * q * (uint32_t)sizeof(XT) : kNowhere);
+        }
+    };
+    float total = 0.0f;
+    fetch(0);
+    for (int s = 0; s < n; s += kStage) {
+        float xv[4], dx[4], gates[4], b[4][NT];
+        // LDS of a wavefront is written and read in its own order
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if constexpr (OUT)
+#pragma unroll
+            for (int i = 0; i < NL; i += 4) {
+                const float f[4] = {next_c[i], next_c[i + 1], next_c[i + 2], next_c[i + 3]};
+                store_vec<4>(&cs[wave][tc][n0 + i], f);
+            }
+        float delta[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            xv[k] = load_one(&next_x[k]);
+            if constexpr (OUT) gates[k] = load_one(&next_z[k]);
+            delta[k] = load_one(&next_dt[k]) + bias;
+#pragma unroll
+            for (int q = 0; q < NT; ++q) b[k][q] = load_one(&next_b[k][q]);
+        }
+        if (a.softplus)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) delta[k] = softplus(delta[k]);
+        if constexpr (OUT)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) gates[k] = a.z ? gate(gates[k]) : 1.0f;
+        if (s + kStage > n)                        // past the last token nothing changes
+#pragma unroll
+            for (int k = 0; k < 4; ++k) delta[k] = s + 4 * k + g < n ? delta[k] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            deltas[wave][k][j][g] = delta[k];
+            dx[k] = delta[k] * xv[k];
+            if (!OUT) total += delta[k];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (s + kStage < n) fetch(s + kStage);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const f32x4 step = *reinterpret_cast<const f32x4 *>(deltas[wave][k][j]);
+            float sum[4] = {};
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                f32x16 add = {};
+                add = __builtin_amdgcn_mfma_f32_16x16x1f32(b[k][q], dx[k], add, 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    f32x4 w = {};
+                    if constexpr (OUT) w = *reinterpret_cast<const f32x4 *>(&cs[wave][4 * k + t][16 * q + 4 * g]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float keep = __builtin_amdgcn_exp2f(step[t] * decay[q][r]);
+                        h[q][r] = fmaf(h[q][r], keep, add[4 * t + r]);
+                        if constexpr (OUT) sum[t] = fmaf(w[r], h[q][r], sum[t]);
+                    }
+                }
+            }
+            if constexpr (OUT) {
+                store_to<XT>(out.from(s + 4 * k, n), off_out, fmaf(skip, xv[k], deal_sums(sum)) * gates[k]);
+            }
+        }
+    }
+    if (!OUT) {
+        to_workspace();
+        total += __shfl_xor(total, 16);
+        a.ws_total[place(seg.index)] = total + __shfl_xor(total, 32);
+        return;
+    }
+    if (seg.last && a.write_state && own)
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+            if (16 * q + 4 * g < a.d_state) store_vec<4>(state + 16 * q, h[q]);
+}
+
+// Between the two: each segment's place in the workspace, which holds what its own tokens leave in a
+// state of zeros, is left with the state behind it, from the row's first state in the last one's place.
+template <int NT>
+__global__ __launch_bounds__(256) void combine(const ScanArgs a) {
+    const int tid = threadIdx.x;
+    const int tile = blockIdx.x % a.tiles, i = blockIdx.x / a.tiles;
+    const int count = uniform(segments_of(a, i));
+    if (count < 2) return;                         // same for the workgroup
+    const int64_t first = first_place<4>(a, i);
+    if (first + count > a.places) return;
+    const int c = tile * kChannels + 16 * (tid >> 6) + (tid & 15), n0 = 4 * (tid >> 4 & 3);
+    if (c >= a.d) return;
+    const int64_t step = (int64_t)a.tiles * 256, at = first * step + tile * 256 + tid;
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+        float rate[4] = {}, h[4];
+        if (16 * q + n0 < a.d_state) load_vec<4>(a.A + (int64_t)c * a.d_state + 16 * q + n0, rate);
+        float *ws = a.ws + at * 4 * NT + 4 * q;
+        load_vec<4>(ws + (count - 1) * step * 4 * NT, h);
+#pragma unroll 4
+        for (int s = 0; s < count - 1; ++s) {
+            const float total = a.ws_total[at + s * step];
+            float add[4];
+            load_vec<4>(ws + s * step * 4 * NT, add);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[r] = fmaf(h[r], __builtin_amdgcn_exp2f(total * (rate[r] * kLog2e)), add[r]);
+            store_vec<4>(ws + s * step * 4 * NT, h);
+        }
+    }
+}
+
+template <typename XT, typename ST, int NT>
+PromptPlan plan() {
+    return {(const void *)prompt<XT, ST, NT, true>, (const void *)prompt<XT, ST, NT, false>, (const void *)combine<NT>,
+            kChannels, 256, kStage, 256 * 4 * NT, 256};
+}
+
+template <typename XT, typename ST>
+PromptPlan pick(int d_state) {
+    if (d_state <= 16) return plan<XT, ST, 1>();
+    if (d_state <= 32) return plan<XT, ST, 2>();
+    if (d_state <= 48) return plan<XT, ST, 3>();
+    return plan<XT, ST, 4>();
+}
+
+}  // namespace
+
+PromptPlan pick_prompt(int x_bytes, int state_bytes, int d_state) {
+    if (x_bytes == 4) return pick<float, float>(d_state);
+    return state_bytes == 4 ? pick<Bf16, float>(d_state) : pick<Bf16, Bf16>(d_state);
+}
+
+}  // namespace sqimpl
