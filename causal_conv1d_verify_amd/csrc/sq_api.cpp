@@ -108,29 +108,33 @@ sqimpl::ScanArgs scan_args(const sq_scan_shape_t *s, const sq_scan_data_t *p, co
 }
 
 // How packed prompts are cut into workgroups: a row's tokens are one chain in one workgroup for each
-// 64 channels unless that chain is much longer than the share of all tokens that each of the chip's
-// slots would have; then rows are cut into segments of about that share, at the price of passing
-// over all but the last of them twice.
+// 64 channels unless few chains leave most of the chip idle; then rows are cut into segments, at the
+// price of passing over all but a row's last one twice.  Eight workgroups for each of 256 compute units
+// take up the cut ones (one prompt of 16384 x 4096: 433 us in segments of 512 tokens, 456 of 1024, 526 of
+// 2048).  Uncut, 256 workgroups take as long (221 us for 2048 tokens; 128: 220, cut 131)
+// and are nearly as fast as in twice the work (cut 211), 384 are as fast (312, cut 308-327); from there
+// on cutting loses (512: 316, cut 401).  Segments of fewer than 64 tokens do not pay for the two
+// launches more (5 rows of up to 333 tokens, 1048 channels: 33.4 us; of 128: 53).
 struct Cut {
     sqimpl::PromptPlan plan;
     int64_t tiles, segments, places, ws_bytes;
     int32_t seg_len;
 };
 Cut cut_prompts(const sq_scan_shape_t *s, int xb, int sb) {
-    constexpr int64_t kSlots = 512;
+    constexpr int64_t kSlots = 2048, kBusy = 320;  // workgroups: of cut rows, and of uncut ones that are left so
     constexpr int64_t kLeast = 4;                  // stages
     Cut c{};
     c.plan = sqimpl::pick_prompt(xb, sb, s->d_state);
     const int64_t stage = c.plan.stage;
-    c.tiles = (s->d + c.plan.channels - 1) / c.plan.channels;
+    c.tiles = ((int64_t)s->d + c.plan.channels - 1) / c.plan.channels;
     c.segments = s->n_seq;
     c.seg_len = s->T;
     int64_t tokens = sat_mul(s->n_seq, s->T);
     if (s->tokens > 0 && s->tokens < tokens) tokens = s->tokens;
     const int64_t chain = (std::min<int64_t>(s->T, tokens) + stage - 1) / stage;
-    const int64_t share = std::max(kLeast, sat_mul(tokens / stage + 1, c.tiles) / kSlots);
+    const int64_t work = sat_mul(tokens / stage + 1, c.tiles), share = std::max(kLeast, work / kSlots);
     const int64_t segments = tokens / (share * stage) + s->n_seq;
-    if (chain > 2 * share + share / 2 && sat_mul(segments, c.tiles) <= INT32_MAX) {
+    if (chain > 2 * kLeast && chain > 2 * share && work / chain < kBusy && sat_mul(segments, c.tiles) <= INT32_MAX) {
         c.seg_len = (int32_t)(share * stage);
         c.segments = segments;
         // only rows of more than seg_len tokens have places in the workspace
@@ -138,6 +142,17 @@ Cut cut_prompts(const sq_scan_shape_t *s, int xb, int sb) {
         c.ws_bytes = sat_mul(sat_mul(c.places, c.tiles), 4 * (c.plan.ws_floats + c.plan.total_floats));
     }
     return c;
+}
+
+// Outputs of 8 and more tokens go in groups of four as prompts do, where a token takes fewer
+// instructions (16 states; 8 rows of 17: 10.2 us for 12.9, 128 rows of 8: 58.5 for 60.2, of 17: 121 for
+// 125, of 32: 164 for 206), with over 32 states of 4 and more (64 rows of 4, 64 states: 32.8 for 36.2, of
+// 8: 38.9 for 65).  For fewer the state's way in counts, which that kernel has in pieces of 16
+// bytes (128 rows of 4: 45 us for 35; 256 rows of 1: 105 for 47 and more), and its 16 states at least (8
+// states, 64 rows of 8: 13 us for 10).
+sqimpl::ScanPlan plan_few(const sq_scan_shape_t *s, const Need &need, int xb, int sb) {
+    if (need.out && s->d_state > 8 && s->T >= (s->d_state > 32 ? 4 : 8)) return sqimpl::pick_groups(xb, sb, s->d_state, s->T);
+    return sqimpl::pick_scan(xb, sb, s->d_state, s->T == 1, need.out);
 }
 
 int few_tokens(const sq_scan_shape_t *s, const sq_scan_data_t *p, const Need &need, const void *state,
@@ -154,8 +169,8 @@ int few_tokens(const sq_scan_shape_t *s, const sq_scan_data_t *p, const Need &ne
                           {"num_tokens", num_tokens, false, 4}};
     if ((rc = check_pointers(ps)) != CV_OK) return rc;
     sqimpl::ScanArgs a = scan_args(s, p, need, state, slot_idx, nullptr, num_tokens, nullptr, out);
-    const sqimpl::ScanPlan plan = sqimpl::pick_scan(xb, sb, s->d_state, need.out);
-    a.tiles = (s->d + plan.channels - 1) / plan.channels;
+    const sqimpl::ScanPlan plan = plan_few(s, need, xb, sb);
+    a.tiles = (int32_t)(((int64_t)s->d + plan.channels - 1) / plan.channels);
     return launch(plan.run, sat_mul(s->n_seq, a.tiles), plan.threads, 0, &a, stream);
 }
 
@@ -297,8 +312,8 @@ int selscan_describe(int call, const sq_scan_shape_t *s, sq_scan_info_t *info) {
         if (c.ws_bytes) info->launches = 3, info->segment_tokens = c.seg_len;
         return CV_OK;
     }
-    const sqimpl::ScanPlan p = sqimpl::pick_scan(xb, sb, s->d_state, need.out);
-    info->workgroups = sat_mul(s->n_seq, (s->d + p.channels - 1) / p.channels);
+    const sqimpl::ScanPlan p = plan_few(s, need, xb, sb);
+    info->workgroups = sat_mul(s->n_seq, ((int64_t)s->d + p.channels - 1) / p.channels);
     info->threads = p.threads;
     info->channels = p.channels;
     return CV_OK;

@@ -29,12 +29,13 @@ struct ScanArgs {
     float *ws_total;              // each channel's sum of delta over each
 };
 
-// Up to 32 tokens of each row (out false: the state only).
+// Up to 32 tokens of each row (one: a single one; out false: the state only).
 struct ScanPlan {
     const void *run;
     int channels, threads;              // of a workgroup
 };
-ScanPlan pick_scan(int x_bytes, int state_bytes, int d_state, bool out);
+ScanPlan pick_scan(int x_bytes, int state_bytes, int d_state, bool one, bool out);
+ScanPlan pick_groups(int x_bytes, int state_bytes, int d_state, int T);
 
 // Packed prompts.  run makes the outputs and the last state; where rows are cut, first leaves what
 // each segment adds to a state of zeros, and the row's first state, in the workspace, and combine

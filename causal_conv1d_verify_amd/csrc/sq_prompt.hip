@@ -62,25 +62,31 @@ __device__ __forceinline__ void store_to(__amdgpu_buffer_rsrc_t r, uint32_t offs
     else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, (int)offset, 0, 0);
 }
 
-// NT: sixteens of states.  OUT: the outputs and the last state; else what each segment of a cut row
-// adds to a state of zeros, and the row's first state, to the workspace.
-template <typename XT, typename ST, int NT, bool OUT>
-__global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
-    constexpr int NP = 16 * NT, NL = 4 * NT;
-    __shared__ alignas(16) float deltas[4][4][16][4];             // [wave][group][channel][token]
-    __shared__ alignas(16) float cs[4][OUT ? kStage : 1][OUT ? NP : 4];
-    __shared__ int64_t found[3];
+// What a launch makes.  PROMPT: the outputs and the last state of packed prompts.  FIRST: what each
+// segment of a cut row adds to a state of zeros, and the row's first state, in the workspace.  FEW: the
+// outputs of up to 32 tokens and, if it is wanted, the state behind them.
+enum { PROMPT, FIRST, FEW };
+
+// NT: sixteens of states; K: groups of four tokens in a stage.
+template <typename XT, typename ST, int NT, int K, int MAKES>
+__global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(const ScanArgs a) {
+    constexpr int NP = 16 * NT, NL = 4 * NT, STAGE = 4 * K;
+    constexpr bool OUT = MAKES == PROMPT || MAKES == FEW, CUTS = MAKES == PROMPT || MAKES == FIRST;
+    __shared__ alignas(16) float deltas[4][K][16][4];             // [wave][group][channel][token]
+    __shared__ alignas(16) float cs[4][OUT ? STAGE : 1][OUT ? NP : 4];
+    __shared__ int64_t found[CUTS ? 3 : 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int j = lane & 15, g = lane >> 4;
     const int tile = uniform((int)(blockIdx.x % a.tiles)), id = uniform((int)(blockIdx.x / a.tiles));
-    const Segment seg = find_segment<4>(a, id, found);
+    Segment seg{id, 0, true, 0};
+    if constexpr (CUTS) seg = find_segment<4>(a, id, found);
     if (seg.row < 0) return;                       // same for the workgroup
     Span row = span_of(a, seg.row);
     row = Span{uniform(row.n), uniform(row.slot), uniform(row.first), uniform(row.seq)};
-    const bool init = !a.has_init || uniform(a.has_init[seg.row]) != 0;
-    const bool cut = !seg.last || seg.index > 0;
-    if (!OUT && !cut) return;
-    if (row.n == 0 && (init || !a.write_state)) return;
+    const bool init = !CUTS || !a.has_init || uniform(a.has_init[seg.row]) != 0;
+    const bool cut = CUTS && (!seg.last || seg.index > 0);
+    if (MAKES == FIRST && !cut) return;
+    if (row.n < 0 || (row.n == 0 && (init || !a.write_state))) return;
     const int c0 = tile * kChannels + 16 * wave;
     if (c0 >= a.d) return;                         // a whole wavefront
     const bool own = c0 + j < a.d;
@@ -111,7 +117,7 @@ __global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
 #pragma unroll
         for (int q = 0; q < NT; ++q) store_vec<4>(ws + 4 * q, h[q]);
     };
-    if (!OUT) {
+    if (MAKES == FIRST) {
         if (seg.last) {                            // the row's first state, in its last place
             if (init) from_pool();
             to_workspace();
@@ -132,8 +138,8 @@ __global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = OUT && a.D ? a.D[c] : 0.0f;
 
     // ---- the tokens
-    const int begin = seg.index * a.seg_len;
-    const int n = row.n - begin < a.seg_len ? row.n - begin : a.seg_len;
+    const int begin = CUTS ? seg.index * a.seg_len : 0;
+    const int n = !CUTS || row.n - begin < a.seg_len ? row.n - begin : a.seg_len;
     const int64_t t0 = row.first + begin;
     auto tokens_of = [&](const void *p, int64_t seq, int64_t tok, int width) {
         return Tokens<XT>{static_cast<const XT *>(p) + row.seq * seq + t0 * tok, (uint32_t)tok, (uint32_t)width};
@@ -144,16 +150,21 @@ __global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
     const uint32_t off_x = own ? x.offset(g, c) : kNowhere, off_dt = own ? dt.offset(g, c) : kNowhere;
     const uint32_t off_z = own ? z.offset(g, c) : kNowhere, off_out = own ? out.offset(g, c) : kNowhere;
     const uint32_t off_b = B.offset(g, j);
-    const int tc = lane >> 2, n0 = (lane & 3) * NL;   // C: the token of the stage and the states that this lane brings
+    const int tc = (lane >> 2) % STAGE, n0 = (lane & 3) * NL;   // C: the token of the stage and the states that this lane brings
     const XT *C = OUT ? static_cast<const XT *>(a.C) + row.seq * a.c_seq + t0 * a.c_tok : nullptr;
-    XT next_x[4], next_dt[4], next_z[4], next_b[4][NT];
+    const uint32_t off_c = tc * (uint32_t)a.c_tok;
+    XT next_x[K], next_dt[K], next_z[K], next_b[K][NT];
     Run<XT, NL> next_c;
     // The stage from token s on.  There is no branch among its loads, which would wait for them:
     // past the row's end x, dt, z and B are 0, and C the last token's, for outputs that nobody has.
     auto fetch = [&](int s) {
-        if constexpr (OUT) next_c.load_near(C + (int64_t)(s + tc < n ? s + tc : n - 1) * a.c_tok, n0, a.d_state);
+        if constexpr (OUT) {
+            uint32_t off = off_c;
+            if (s + STAGE > n) off = (uint32_t)(s + tc < n ? tc : n - 1 - s) * (uint32_t)a.c_tok;
+            next_c.load(C + s * a.c_tok + off, n0, a.d_state);
+        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < K; ++k) {
             const int s4 = s + 4 * k;
             next_x[k] = load_from<XT>(x.from(s4, n), off_x);
             next_dt[k] = load_from<XT>(dt.from(s4, n), off_dt);
@@ -166,8 +177,8 @@ __global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
     };
     float total = 0.0f;
     fetch(0);
-    for (int s = 0; s < n; s += kStage) {
-        float xv[4], dx[4], gates[4], b[4][NT];
+    for (int s = 0; s < n; s += STAGE) {
+        float xv[K], dx[K], gates[K], b[K][NT];
         // LDS of a wavefront is written and read in its own order
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if constexpr (OUT)
@@ -176,9 +187,9 @@ __global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
                 const float f[4] = {next_c[i], next_c[i + 1], next_c[i + 2], next_c[i + 3]};
                 store_vec<4>(&cs[wave][tc][n0 + i], f);
             }
-        float delta[4];
+        float delta[K];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < K; ++k) {
             xv[k] = load_one(&next_x[k]);
             if constexpr (OUT) gates[k] = load_one(&next_z[k]);
             delta[k] = load_one(&next_dt[k]) + bias;
@@ -187,24 +198,25 @@ __global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
         }
         if (a.softplus)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) delta[k] = softplus(delta[k]);
+            for (int k = 0; k < K; ++k) delta[k] = softplus(delta[k]);
         if constexpr (OUT)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) gates[k] = a.z ? gate(gates[k]) : 1.0f;
-        if (s + kStage > n)                        // past the last token nothing changes
+            for (int k = 0; k < K; ++k) gates[k] = a.z ? gate(gates[k]) : 1.0f;
+        if (s + STAGE > n)                        // past the last token nothing changes
 #pragma unroll
-            for (int k = 0; k < 4; ++k) delta[k] = s + 4 * k + g < n ? delta[k] : 0.0f;
+            for (int k = 0; k < K; ++k) delta[k] = s + 4 * k + g < n ? delta[k] : 0.0f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < K; ++k) {
             deltas[wave][k][j][g] = delta[k];
             dx[k] = delta[k] * xv[k];
-            if (!OUT) total += delta[k];
+            if (MAKES == FIRST) total += delta[k];
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (s + kStage < n) fetch(s + kStage);
+        if (s + STAGE < n) fetch(s + STAGE);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < K; ++k) {
+            if (!CUTS && s + 4 * k >= n) break;    // (prompts: no branch; tokens past the end change nothing)
             const f32x4 step = *reinterpret_cast<const f32x4 *>(deltas[wave][k][j]);
             float sum[4] = {};
 #pragma unroll
@@ -228,7 +240,7 @@ __global__ __launch_bounds__(256, 4) void prompt(const ScanArgs a) {
             }
         }
     }
-    if (!OUT) {
+    if (MAKES == FIRST) {
         to_workspace();
         total += __shfl_xor(total, 16);
         a.ws_total[place(seg.index)] = total + __shfl_xor(total, 32);
@@ -273,8 +285,12 @@ __global__ __launch_bounds__(256) void combine(const ScanArgs a) {
 
 template <typename XT, typename ST, int NT>
 PromptPlan plan() {
-    return {(const void *)prompt<XT, ST, NT, true>, (const void *)prompt<XT, ST, NT, false>, (const void *)combine<NT>,
-            kChannels, 256, kStage, 256 * 4 * NT, 256};
+    return {(const void *)prompt<XT, ST, NT, 4, PROMPT>, (const void *)prompt<XT, ST, NT, 4, FIRST>, (const void *)combine<NT>,
+            kChannels, 256, 16, 256 * 4 * NT, 256};
+}
+template <typename XT, typename ST, int NT>
+ScanPlan plan_few(int T) {
+    return {T <= 8 ? (const void *)prompt<XT, ST, NT, 2, FEW> : (const void *)prompt<XT, ST, NT, 4, FEW>, kChannels, 256};
 }
 
 template <typename XT, typename ST>
@@ -284,12 +300,23 @@ PromptPlan pick(int d_state) {
     if (d_state <= 48) return plan<XT, ST, 3>();
     return plan<XT, ST, 4>();
 }
+template <typename XT, typename ST>
+ScanPlan pick_few(int d_state, int T) {
+    if (d_state <= 16) return plan_few<XT, ST, 1>(T);
+    if (d_state <= 32) return plan_few<XT, ST, 2>(T);
+    if (d_state <= 48) return plan_few<XT, ST, 3>(T);
+    return plan_few<XT, ST, 4>(T);
+}
 
 }  // namespace
 
 PromptPlan pick_prompt(int x_bytes, int state_bytes, int d_state) {
     if (x_bytes == 4) return pick<float, float>(d_state);
     return state_bytes == 4 ? pick<Bf16, float>(d_state) : pick<Bf16, Bf16>(d_state);
+}
+ScanPlan pick_groups(int x_bytes, int state_bytes, int d_state, int T) {
+    if (x_bytes == 4) return pick_few<float, float>(d_state, T);
+    return state_bytes == 4 ? pick_few<Bf16, float>(d_state, T) : pick_few<Bf16, Bf16>(d_state, T);
 }
 
 }  // namespace sqimpl

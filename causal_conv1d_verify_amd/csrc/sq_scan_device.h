@@ -20,54 +20,40 @@ typedef uint32_t u32x2_2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x2_4 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// NL consecutive elements as they lie in memory, the ones from `left` on as 0.  (NL a multiple of 4:
-// `left` is one too.  Else all are there.)
+// The NL consecutive elements from n0 on of a row of `count` (a multiple of 8), as they lie in memory.
+// Quads past the row (there are some only where NL is over 8) are 0, and what is loaded for them the
+// row's first: no branch among loads.
 template <typename XT, int NL>
 struct Run {
     static constexpr int W = NL * (int)sizeof(XT) / 4;
+    static constexpr bool kWhole = NL <= 8;
     uint32_t w[W];
-    __device__ __forceinline__ void load(const XT *p, int left) {
+    __device__ __forceinline__ void load(const XT *row, int n0, int count) {
         if constexpr (NL % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < NL; i += 4)
+            for (int i = 0; i < NL; i += 4) {
+                const bool in = kWhole || n0 + i < count;
+                const XT *p = row + (in ? n0 + i : 0);
                 if constexpr (sizeof(XT) == 2) {
-                    u32x2_2 v = {0, 0};
-                    if (i < left) v = *reinterpret_cast<const u32x2_2 *>(p + i);
-                    w[i / 2] = v[0], w[i / 2 + 1] = v[1];
+                    const u32x2_2 v = load_as<false, u32x2_2>(p);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) w[i / 2 + e] = in ? v[e] : 0;
                 } else {
-                    u32x4_4 v = {0, 0, 0, 0};
-                    if (i < left) v = *reinterpret_cast<const u32x4_4 *>(p + i);
-                    w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
+                    const u32x4_4 v = load_as<false, u32x4_4>(p);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[i + e] = in ? v[e] : 0;
                 }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < NL; i += 2)
                 if constexpr (sizeof(XT) == 2) {
-                    w[i / 2] = (*reinterpret_cast<const u32_2 *>(p + i))[0];
+                    w[i / 2] = load_as<false, u32_2>(row + n0 + i)[0];
                 } else {
-                    const u32x2_4 v = *reinterpret_cast<const u32x2_4 *>(p + i);
+                    const u32x2_4 v = load_as<false, u32x2_4>(row + n0 + i);
                     w[i] = v[0], w[i + 1] = v[1];
                 }
         }
-    }
-    // The run from n0 on of a row of `count`; quads past the row are its first one instead.
-    __device__ __forceinline__ void load_near(const XT *row, int n0, int count) {
-        static_assert(NL % 4 == 0);
-#pragma unroll
-        for (int i = 0; i < NL; i += 4) {
-            const XT *p = row + (n0 + i < count ? n0 + i : 0);
-            if constexpr (sizeof(XT) == 2) {
-                const u32x2_2 v = *reinterpret_cast<const u32x2_2 *>(p);
-                w[i / 2] = v[0], w[i / 2 + 1] = v[1];
-            } else {
-                const u32x4_4 v = *reinterpret_cast<const u32x4_4 *>(p);
-                w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
-            }
-        }
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = 0;
     }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (sizeof(XT) == 2) return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
@@ -75,19 +61,20 @@ struct Run {
     }
 };
 
+// A state's run back, `left` of it.
 template <typename ST, int NL>
 __device__ __forceinline__ void store_run(ST *p, const float (&h)[NL], int left) {
     if constexpr (NL % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < NL; i += 4) {
             const float f[4] = {h[i], h[i + 1], h[i + 2], h[i + 3]};
-            if (i < left) store_vec<4>(p + i, f);
+            if (NL <= 8 || i < left) store_vec<4>(p + i, f);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NL; i += 2)
-            if constexpr (sizeof(ST) == 2) *reinterpret_cast<uint32_t *>(p + i) = pack_bf16(h[i], h[i + 1]);
-            else *reinterpret_cast<u32x2 *>(p + i) = u32x2{__float_as_uint(h[i]), __float_as_uint(h[i + 1])};
+            if constexpr (sizeof(ST) == 2) store_as<false>(p + i, pack_bf16(h[i], h[i + 1]));
+            else store_as<false>(p + i, u32x2{__float_as_uint(h[i]), __float_as_uint(h[i + 1])});
     }
 }
 
@@ -102,7 +89,7 @@ __device__ __forceinline__ float softplus(float v) {
     p = fmaf(p, s2, 0.40025115f);
     p = fmaf(p, s2, 0.6666631f);
     p = fmaf(p, s2, 2.0f);
-    return fmaf(p, s, __builtin_amdgcn_fmed3f(v, 0.0f, INFINITY));
+    return fmaf(p, s, __int_as_float(max(__float_as_int(v), 0)));   // (and NaN stays)
 }
 
 // z / (1 + 2^(-z log2 e)).  Where its sigmoid is below fp32's normal range (z under -87) it is 0.
