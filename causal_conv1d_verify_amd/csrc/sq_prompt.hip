@@ -159,9 +159,9 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
     // past the row's end x, dt, z and B are 0, and C the last token's, for outputs that nobody has.
     auto fetch = [&](int s) {
         if constexpr (OUT) {
-            uint32_t off = off_c;
-            if (s + STAGE > n) off = (uint32_t)(s + tc < n ? tc : n - 1 - s) * (uint32_t)a.c_tok;
-            next_c.load(C + s * a.c_tok + off, n0, a.d_state);
+            const XT *p = C + s * a.c_tok + off_c;
+            if (s + STAGE > n) p = C + (int64_t)(s + tc < n ? s + tc : n - 1) * a.c_tok;
+            next_c.load(p, n0, a.d_state);
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -177,6 +177,9 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
     };
     float total = 0.0f;
     fetch(0);
+    // The first stage's loads are waited for here: with none under way into the loop, its own wait is for
+    // a stage's loads alone and not for the stores behind them.
+    if (CUTS) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
     for (int s = 0; s < n; s += STAGE) {
         float xv[K], dx[K], gates[K], b[K][NT];
         // LDS of a wavefront is written and read in its own order
@@ -201,7 +204,10 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
             for (int k = 0; k < K; ++k) delta[k] = softplus(delta[k]);
         if constexpr (OUT)
 #pragma unroll
-            for (int k = 0; k < K; ++k) gates[k] = a.z ? gate(gates[k]) : 1.0f;
+            for (int k = 0; k < K; ++k) {
+                const float open = gate(gates[k]);   // (without z that of x, which nobody has)
+                gates[k] = a.z ? open : 1.0f;
+            }
         if (s + STAGE > n)                        // past the last token nothing changes
 #pragma unroll
             for (int k = 0; k < K; ++k) delta[k] = s + 4 * k + g < n ? delta[k] : 0.0f;
@@ -213,7 +219,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (s + STAGE < n) fetch(s + STAGE);
+        if (CUTS || s + STAGE < n) fetch(s + STAGE);   // (past the row's end: no bytes)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (!CUTS && s + 4 * k >= n) break;    // (prompts: no branch; tokens past the end change nothing)

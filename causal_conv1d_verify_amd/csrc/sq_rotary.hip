@@ -53,11 +53,47 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
+// 1 / sqrt(sum / dim + eps) of a head's squares.  A head whose sum leaves fp32's range is scaled by a
+// power of two and summed again.
+template <int LG>
+__device__ __forceinline__ float inverse_norm(float (&v)[16], float per_dim, float eps) {
+    auto total = [&]() {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s = fmaf(v[j], v[j], s);
+        return group_sum<LG>(s);
+    };
+    float sum = total(), e = eps;
+    const bool high = !(sum < INFINITY), low = sum < 0x1p-100f && eps < 0x1p-100f;
+    if (__builtin_expect(high || low, 0)) {
+        const float scale = high ? 0x1p-80f : 0x1p80f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= scale;
+        sum = total();
+        e = (eps * scale) * scale;
+    }
+    return __builtin_amdgcn_rsqf(fmaf(sum, per_dim, e));
+}
+
+// Eight channels as they lie in memory.
+template <typename XT>
+struct Eight {
+    u32x4 w[sizeof(XT) / 2];
+    __device__ __forceinline__ void load(const XT *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(XT) / 2; ++i) w[i] = reinterpret_cast<const u32x4 *>(p)[i];
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        if constexpr (sizeof(XT) == 2) return j & 1 ? bf16_hi(w[0][j / 2]) : bf16_lo(w[0][j / 2]);
+        else return __uint_as_float(w[j / 4][j % 4]);
+    }
+};
+
 template <typename XT, int LG>
 __global__ __launch_bounds__(256) void rotary(const RotaryArgs a) {
     constexpr int SIDE = kWave / LG;               // heads side by side
     constexpr int BATCH = 4;                       // of each lane, in flight at once
-    __shared__ float cs[4][2][128];
+    __shared__ alignas(16) float cs[4][2][128];
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     const int64_t id = (int64_t)blockIdx.x * 4 + wave;
     const int64_t token = id / a.blocks_per_token;
@@ -66,8 +102,8 @@ __global__ __launch_bounds__(256) void rotary(const RotaryArgs a) {
     const int heads = a.heads[0] + a.heads[1], units = a.dim / 16, turned = a.rot / 16;
     const int u = lane % LG;
     const bool in = u < units, turns = u < turned;
-    const int c0 = a.interleaved || !turns ? 16 * u : 8 * u;
-    const int c1 = a.interleaved || !turns ? c0 + 8 : c0 + a.rot / 2;
+    // both halves of what is rotated, and of what is not
+    const int c0 = turns ? 8 * u : a.rot + 8 * (u - turned), c1 = c0 + (turns ? a.rot : a.dim - a.rot) / 2;
     const int first = part * SIDE + lane / LG, step = a.blocks_per_token * SIDE;
 
     const XT *from[2];
@@ -77,19 +113,17 @@ __global__ __launch_bounds__(256) void rotary(const RotaryArgs a) {
         from[i] = static_cast<const XT *>(a.x[i]) + token * a.tok[i];
         to[i] = static_cast<XT *>(a.out[i]) + token * a.out_tok[i];
     }
-    float v[BATCH][16];
+    Eight<XT> raw[BATCH][2];
     auto load = [&](int h0) {
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             const int h = h0 + b * step, i = h >= a.heads[0];
-            float lo[8] = {}, hi[8] = {};
+            raw[b][0] = raw[b][1] = Eight<XT>{};
             if (in && h < heads) {
                 const XT *p = (i ? from[1] : from[0]) + (h - (i ? a.heads[0] : 0)) * (i ? a.head[1] : a.head[0]);
-                load_vec<8>(p + c0, lo);
-                load_vec<8>(p + c1, hi);
+                raw[b][0].load(p + c0);
+                raw[b][1].load(p + c1);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[b][j] = lo[j], v[b][8 + j] = hi[j];
         }
     };
     load(first);
@@ -106,60 +140,66 @@ __global__ __launch_bounds__(256) void rotary(const RotaryArgs a) {
     }
     float cos[8], sin[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cos[j] = 1.0f, sin[j] = 0.0f;
+    for (int j = 0; j < 8; ++j) cos[j] = sin[j] = 0.0f;
     if (turns) {
-        load_vec<8>(&cs[wave][0][8 * u], cos);
-        load_vec<8>(&cs[wave][1][8 * u], sin);
+        // pairs 8u to 8u + 7, or of neighbours those of either half
+        const int p0 = a.interleaved ? 4 * u : 8 * u, p1 = a.interleaved ? 4 * u + a.rot / 4 : 8 * u + 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            cos[j] = cs[wave][0][p0 + j], cos[4 + j] = cs[wave][0][p1 + j];
+            sin[j] = cs[wave][1][p0 + j], sin[4 + j] = cs[wave][1][p1 + j];
+        }
     }
 
+    const float per_dim = 1.0f / (float)a.dim;
     for (int h0 = first; h0 - lane / LG < heads; h0 += BATCH * step) {
         if (h0 != first) load(h0);
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             const int h = h0 + b * step, i = h >= a.heads[0];
             const XT *w = static_cast<const XT *>(i ? a.weight[1] : a.weight[0]);
-            float mult = 1.0f, pre = 1.0f;
-            inverse_rms([&](float scale) {
-                float s = 0.0f;
+            float v[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s = fmaf(v[b][j] * scale, v[b][j] * scale, s);
-                return group_sum<LG>(s);
-            }, a.dim, a.eps, mult, pre);
+            for (int j = 0; j < 8; ++j) v[j] = raw[b][0][j], v[8 + j] = raw[b][1][j];
+            if (w) {                               // the same for a head's lanes
+                const float mult = inverse_norm<LG>(v, per_dim, a.eps);
+                float f[16] = {};
+                if (in) {
+                    float lo[8], hi[8];
+                    load_vec<8>(w + c0, lo);
+                    load_vec<8>(w + c1, hi);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = lo[j], f[8 + j] = hi[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = (v[j] * mult) * f[j];
+            }
             if (!in || h >= heads) continue;
             float lo[8], hi[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) lo[j] = v[b][j], hi[j] = v[b][8 + j];
-            if (w) {
-                float f[8];
-                load_vec<8>(w + c0, f);
+            for (int j = 0; j < 8; ++j) lo[j] = v[j], hi[j] = v[8 + j];
+            if (turns && a.interleaved) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) lo[j] = ((lo[j] * pre) * mult) * f[j];
-                load_vec<8>(w + c1, f);
+                for (int j = 0; j < 4; ++j) {
+                    const float e = lo[2 * j], f = lo[2 * j + 1], g = hi[2 * j], k = hi[2 * j + 1];
+                    lo[2 * j] = fmaf(e, cos[j], -(f * sin[j]));
+                    lo[2 * j + 1] = fmaf(f, cos[j], e * sin[j]);
+                    hi[2 * j] = fmaf(g, cos[4 + j], -(k * sin[4 + j]));
+                    hi[2 * j + 1] = fmaf(k, cos[4 + j], g * sin[4 + j]);
+                }
+            } else if (turns) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) hi[j] = ((hi[j] * pre) * mult) * f[j];
-            }
-            if (turns) {
-                if (a.interleaved) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float e = lo[2 * j], f = lo[2 * j + 1], g = hi[2 * j], k = hi[2 * j + 1];
-                        lo[2 * j] = fmaf(e, cos[j], -(f * sin[j]));
-                        lo[2 * j + 1] = fmaf(f, cos[j], e * sin[j]);
-                        hi[2 * j] = fmaf(g, cos[4 + j], -(k * sin[4 + j]));
-                        hi[2 * j + 1] = fmaf(k, cos[4 + j], g * sin[4 + j]);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float e = lo[j], f = hi[j];
-                        lo[j] = fmaf(e, cos[j], -(f * sin[j]));
-                        hi[j] = fmaf(f, cos[j], e * sin[j]);
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    const float e = lo[j], f = hi[j];
+                    lo[j] = fmaf(e, cos[j], -(f * sin[j]));
+                    hi[j] = fmaf(f, cos[j], e * sin[j]);
                 }
             }
             XT *p = (i ? to[1] : to[0]) + (h - (i ? a.heads[0] : 0)) * (i ? a.out_head[1] : a.out_head[0]);
-            store_vec<8>(p + c0, lo);
-            store_vec<8>(p + c1, hi);
+            // past the caches' usual order: alone 4-20% faster (16384 tokens of 32 heads of 128: 54.4 us for
+            // 58.4), with a reader behind it from 6% faster to 5% slower
+            store_vec<8, true>(p + c0, lo);
+            store_vec<8, true>(p + c1, hi);
         }
     }
 }
