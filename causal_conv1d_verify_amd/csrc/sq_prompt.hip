@@ -271,20 +271,29 @@ __global__ __launch_bounds__(256) void combine(const ScanArgs a) {
     const int c = tile * kChannels + 16 * (tid >> 6) + (tid & 15), n0 = 4 * (tid >> 4 & 3);
     if (c >= a.d) return;
     const int64_t step = (int64_t)a.tiles * 256, at = first * step + tile * 256 + tid;
+    constexpr int AHEAD = 8;                       // segments that are in flight at once
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
         float rate[4] = {}, h[4];
         if (16 * q + n0 < a.d_state) load_vec<4>(a.A + (int64_t)c * a.d_state + 16 * q + n0, rate);
         float *ws = a.ws + at * 4 * NT + 4 * q;
         load_vec<4>(ws + (count - 1) * step * 4 * NT, h);
-#pragma unroll 4
-        for (int s = 0; s < count - 1; ++s) {
-            const float total = a.ws_total[at + s * step];
-            float add[4];
-            load_vec<4>(ws + s * step * 4 * NT, add);
+        for (int s0 = 0; s0 < count - 1; s0 += AHEAD) {
+            float add[AHEAD][4], total[AHEAD];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) h[r] = fmaf(h[r], __builtin_amdgcn_exp2f(total * (rate[r] * kLog2e)), add[r]);
-            store_vec<4>(ws + s * step * 4 * NT, h);
+            for (int u = 0; u < AHEAD; ++u) {
+                const int64_t s = s0 + u < count - 1 ? s0 + u : count - 2;
+                load_vec<4>(ws + s * step * 4 * NT, add[u]);
+                total[u] = a.ws_total[at + s * step];
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (s0 + u < count - 1) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        h[r] = fmaf(h[r], __builtin_amdgcn_exp2f(total[u] * (rate[r] * kLog2e)), add[u][r]);
+                    store_vec<4>(ws + (s0 + u) * step * 4 * NT, h);
+                }
         }
     }
 }
