@@ -26,6 +26,20 @@ int check_strides(const Stride *strides, int n) {
     return CV_OK;
 }
 
+// The name of a stride over which sq_prompt.hip's 32-bit offsets do not reach: of four tokens, of C a
+// stage; NULL if they do.
+const char *far_tokens(const sq_scan_shape_t *s, bool out) {
+    const int64_t most = INT32_MAX / 4;
+    const struct { const char *name; int64_t stride; int tokens; bool used; } strides[] = {
+        {"x_tok_stride", s->x_tok_stride, 3, true}, {"dt_tok_stride", s->dt_tok_stride, 3, true},
+        {"z_tok_stride", s->z_tok_stride, 3, out}, {"b_tok_stride", s->b_tok_stride, 3, true},
+        {"c_tok_stride", s->c_tok_stride, 15, out}, {"out_tok_stride", s->out_tok_stride, 3, out},
+    };
+    for (const auto &d : strides)
+        if (d.used && sat_add(sat_mul(d.tokens, d.stride), std::max(s->d, 64)) > (dtype_bytes(s->x_dtype) == 4 ? most : 2 * most)) return d.name;
+    return nullptr;
+}
+
 // What every entry point of the scan checks; *empty: there is nothing to do.
 int check_scan(const sq_scan_shape_t *s, const Need &need, int *xb, int *sb, bool *empty) {
     if (!s) return fail(CV_EINVAL, "shape is NULL");
@@ -66,12 +80,8 @@ int check_scan(const sq_scan_shape_t *s, const Need &need, int *xb, int *sb, boo
         Dim d[2] = {{toks, s->out_tok_stride}, {rows ? s->n_seq : 1, s->out_seq_stride}};
         if (!apart(s->d, d, 2)) return fail(CV_EINVAL, "the strides of out make its rows overlap");
     }
-    if (need.packed)
-        for (const Stride &d : {Stride{"x_tok_stride", s->x_tok_stride, true, 0}, {"dt_tok_stride", s->dt_tok_stride, true, 0},
-                                {"z_tok_stride", s->z_tok_stride, true, 0}, {"b_tok_stride", s->b_tok_stride, true, 0},
-                                {"out_tok_stride", s->out_tok_stride, true, 0}})
-            if (sat_add(sat_mul(3, d.stride), s->d) > INT32_MAX / *xb)
-                return fail(CV_ENOTSUP, "%s (%lld): four tokens span more than 2 GiB", d.name, (long long)d.stride);
+    if (const char *far = need.packed ? far_tokens(s, true) : nullptr)
+        return fail(CV_ENOTSUP, "%s: four tokens (of C: 16) span more than 2 GiB", far);
     *empty = s->n_seq == 0;
     return CV_OK;
 }
@@ -149,9 +159,9 @@ Cut cut_prompts(const sq_scan_shape_t *s, int xb, int sb) {
 // 125, of 32: 164 for 206), with over 32 states of 4 and more (64 rows of 4, 64 states: 32.8 for 36.2, of
 // 8: 38.9 for 65).  For fewer the state's way in counts, which that kernel has in pieces of 16
 // bytes (128 rows of 4: 45 us for 35; 256 rows of 1: 105 for 47 and more), and its 16 states at least (8
-// states, 64 rows of 8: 13 us for 10).
+// states, 64 rows of 8: 13 us for 10).  Tokens too far apart for its offsets go the other way too.
 sqimpl::ScanPlan plan_few(const sq_scan_shape_t *s, const Need &need, int xb, int sb) {
-    if (need.out && s->d_state > 8 && s->T >= (s->d_state > 32 ? 4 : 8)) return sqimpl::pick_groups(xb, sb, s->d_state, s->T);
+    if (need.out && s->d_state > 8 && s->T >= (s->d_state > 32 ? 4 : 8) && !far_tokens(s, true)) return sqimpl::pick_groups(xb, sb, s->d_state, s->T);
     return sqimpl::pick_scan(xb, sb, s->d_state, s->T == 1, need.out);
 }
 

@@ -53,7 +53,8 @@ extern "C" {
  *    that write are distinct; cu_seqlens stays inside the token buffers.
  *  - Supported (else CV_ENOTSUP): d a multiple of 8; d_state a multiple of 8, 8..64; (x, state)
  *    types (F32, F32), (BF16, BF16), (BF16, F32); x, dt, z, out, A, D, dt_bias and the state 16-byte
- *    aligned, their strides multiples of 16 bytes; B and C aligned to their elements.
+ *    aligned, their strides multiples of 16 bytes; B and C aligned to their elements; prefill: any four
+ *    tokens of x, dt, z, B and out, and any 16 of C, within 2 GiB.
  *  - Numerics: delta, decays, states and sums are held in fp32.  A state stored as bf16 is rounded
  *    once, after the last token of the call.  A token's values that are not finite change the
  *    outputs of their own and of later tokens only (x, dt, z: of their own channel).

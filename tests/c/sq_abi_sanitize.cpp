@@ -124,10 +124,12 @@ void scan_accepted(int call, const sq_scan_shape_t &s) {
         check((wide)l.grid == (wide)(l.code == 4 ? s.n_seq : a.segments) * a.tiles, "workgroups");
     }
     check(g_launches.back().code == (call == SQ_SCAN_PREFILL ? 2 : g_launches.back().code == 1 ? 1 : 0), "kernel");
+    if (g_launches.back().code >= 1) {             // four tokens lie within 2 GiB, and 16 of C
+        const int xb = s.x_dtype == CV_F32 ? 4 : 2;
+        for (int64_t t : {a.x_tok, a.dt_tok, a.z_tok, a.o_tok, a.b_tok, 5 * a.c_tok})
+            check(((wide)3 * t + s.d) * xb <= INT32_MAX, "far tokens");
+    }
     if (call != SQ_SCAN_PREFILL) return;
-    // four tokens of each lie within 2 GiB
-    const int xb = s.x_dtype == CV_F32 ? 4 : 2;
-    for (int64_t t : {a.x_tok, a.dt_tok, a.z_tok, a.o_tok, a.b_tok}) check(((wide)3 * t + s.d) * xb <= INT32_MAX, "far tokens");
     if (info.launches != 3) {
         check(a.seg_len == s.T && a.segments == s.n_seq && info.workspace_bytes == 0, "whole rows");
         return;

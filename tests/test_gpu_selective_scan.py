@@ -341,3 +341,62 @@ def test_rows_past_32_bit_offsets():
     prefill(q)
     torch.cuda.synchronize()
     assert torch.equal(p.out, q.out) and torch.equal(p.pool_full, q.pool_full)
+
+
+def test_few_tokens_too_far_apart():
+    """Token rows 2^29 elements apart, past the 32-bit offsets of the kernel that takes near ones."""
+    _say("few far rows")
+    cv = _cv()
+    far = 2 ** 29
+    for kind in ("verify", "update"):
+        p, q = (Problem([9] * 2, 64, 16, "bf16_f32", packed=False, T=9) for _ in range(2))
+        wide = torch.empty(8 * far + 2 * 64, dtype=BF16, device="cuda")
+        view = torch.as_strided(wide, (2, 9, 64), (64, far, 1))
+        view.copy_(p.x)
+        p.x = view
+        want = q.expect(writes=kind == "update")
+        for r in (p, q):
+            getattr(cv, "selective_scan_" + kind)(r.x, r.dt, r.A, r.B, r.C, r.pool, r.out, **r.kw())
+            r.check(want)
+
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_inputs_that_are_broadcast(packed):
+    """One dt, z, B and C for all tokens (stride 0)."""
+    _say("broadcast", packed)
+    cv = _cv()
+    p = Problem([21] * 3, 72, 16, "bf16_f32", packed=packed, T=21)
+    for name in ("dt", "z", "B", "C"):
+        t = getattr(p, name)
+        first = t[:1] if packed else t[:, :1]
+        setattr(p, name, first.expand_as(t))
+    want = p.expect()
+    if packed:
+        prefill(p)
+    else:
+        cv.selective_scan_update(p.x, p.dt, p.A, p.B, p.C, p.pool, p.out, **p.kw())
+    p.check(want)
+
+
+def test_tokens_behind_the_last_row_are_left():
+    _say("tail")
+    p = Problem([30, 17, 9], 72, 16, "bf16_f32", packed=True)
+    p.cu = p.cu[:-1].contiguous()
+    p.rows, p.lengths, p.slots = 2, p.lengths[:2], p.slots[:2].contiguous()
+    want = p.expect()
+    prefill(p)
+    p.check(want)
+
+
+def test_two_calls_at_once():
+    """Cut prompts on two streams, each with a workspace of its own."""
+    _say("two streams")
+    ps = [Problem([1200, 40], 72, 16, "bf16_f32", packed=True, seed=k) for k in range(2)]
+    wants = [p.expect() for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for p, s in zip(ps, streams):
+        with torch.cuda.stream(s):
+            prefill(p)
+    for p, want in zip(ps, wants):
+        p.check(want)

@@ -104,7 +104,7 @@ for name, kw in dict(z_unaligned=dict(z_tok_stride=68), out_unaligned=dict(out_t
 update("out_rows", shape(out_seq_stride=64)); verify("out_rows", shape(out_seq_stride=64))
 for f in (update, verify, commit):
     f("T33", shape(T=33))
-for name in ("x", "dt", "z", "b", "out"):
+for name in ("x", "dt", "z", "b", "c", "out"):
     prefill("far_" + name, shape(T=100, **{name + "_tok_stride": 1 << 30}))
 for f in ALL:
     for p in ("x", "dt", "A", "B"):
@@ -229,6 +229,21 @@ def test_descriptions():
         assert rc == 0, lib.seqops_last_error()
         return got
 
+    def far(call, **kw):
+        """The channels of a workgroup where some tokens are too far apart for 32-bit offsets."""
+        d = dict(n_seq=1, T=8, d=64, d_state=16, x_dtype=base.CV_BF16, state_dtype=base.CV_F32, n_slots=1, softplus=1,
+                 x_tok_stride=64, dt_tok_stride=64, z_tok_stride=64, out_tok_stride=64, b_tok_stride=16, c_tok_stride=16)
+        d.update(kw)
+        got = sq.SqScanInfo()
+        assert lib.selscan_describe(call, sq.SqScanShape(**d), ctypes.byref(got)) == 0
+        return got.channels
+
+    assert far(sq.SQ_SCAN_VERIFY) == 64
+    for name in ("x", "dt", "z", "b", "out"):
+        near = (2 ** 30 - 1 - 64) // 3 // 8 * 8    # elements of bf16
+        assert far(sq.SQ_SCAN_VERIFY, **{name + "_tok_stride": near}) == 64
+        assert far(sq.SQ_SCAN_VERIFY, **{name + "_tok_stride": near + 8}) == 256
+    assert far(sq.SQ_SCAN_UPDATE, c_tok_stride=2 ** 26) == 64 and far(sq.SQ_SCAN_UPDATE, c_tok_stride=2 ** 27) == 256
     one = info(sq.SQ_SCAN_UPDATE, T=1)
     assert (one.launches, one.channels, one.workgroups) == (1, 256, 4 * 32)
     assert info(sq.SQ_SCAN_VERIFY).channels == 64 and info(sq.SQ_SCAN_COMMIT).channels == 256
