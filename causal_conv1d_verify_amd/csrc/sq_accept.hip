@@ -152,9 +152,23 @@ struct Weights {
     }
 };
 
-__device__ __forceinline__ double wave_sum(double s) {
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d /= 2) s += __shfl_xor(s, d);
+// The value of the lane that CTRL names, in the rows that ROWS has, and 0 in others: DPP moves, a few
+// cycles each where a shuffle through LDS takes some sixty.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// The running sums over a wavefront: of each row of 16 lanes, then with the rows before.
+__device__ __forceinline__ double wave_upto(double s) {
+    s += moved<0x111, 0xF>(s);    // the lane before
+    s += moved<0x112, 0xF>(s);    // two, four and eight before
+    s += moved<0x114, 0xF>(s);
+    s += moved<0x118, 0xF>(s);
+    s += moved<0x142, 0xA>(s);    // the last of the row before, in the second and the fourth
+    s += moved<0x143, 0xC>(s);    // the last of the second, in the third and the fourth
     return s;
 }
 
@@ -175,7 +189,7 @@ __device__ __forceinline__ double part_sum(const Weights<PT> &weights, int part)
         if (slow) weights.take_removed(begin + 4 * (lane + kWave * k), w);
         s += (w[0] + w[1]) + (w[2] + w[3]);
     }
-    return wave_sum(s);
+    return lane_value(wave_upto(s), kWave - 1);
 }
 
 template <typename PT>
@@ -196,12 +210,7 @@ __global__ __launch_bounds__(256) void sums(const AcceptArgs a) {
 // The running sums of each lane's `own` over the workgroup's 256 lanes: what is before it, and all.
 __device__ __forceinline__ double before_lane(double own, double *waves, double &all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double upto = own;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const double y = __shfl_up(upto, d);
-        if (lane >= d) upto += y;
-    }
+    const double upto = wave_upto(own), y = moved<0x138, 0xF>(upto);   // (of the lane before)
     __syncthreads();                               // the last sums are read
     if (lane == kWave - 1) waves[wave] = upto;
     __syncthreads();
@@ -212,8 +221,7 @@ __device__ __forceinline__ double before_lane(double own, double *waves, double 
         if (w < wave) base += waves[w];
         all += waves[w];
     }
-    const double y = __shfl_up(upto, 1);
-    return base + (lane ? y : 0.0);
+    return base + y;
 }
 
 // Of the workgroup's lanes in order, the value of the first that has one, and that of the last that
