@@ -119,12 +119,17 @@ sqimpl::ScanArgs scan_args(const sq_scan_shape_t *s, const sq_scan_data_t *p, co
 
 // How packed prompts are cut into workgroups: a row's tokens are one chain in one workgroup for each
 // 64 channels unless few chains leave most of the chip idle; then rows are cut into segments, at the
-// price of passing over all but a row's last one twice.  Eight workgroups for each of 256 compute units
-// take up the cut ones (one prompt of 16384 x 4096: 433 us in segments of 512 tokens, 456 of 1024, 526 of
-// 2048).  Uncut, 256 workgroups take as long (221 us for 2048 tokens; 128: 220, cut 131)
-// and are nearly as fast as in twice the work (cut 211), 384 are as fast (312, cut 308-327); from there
-// on cutting loses (512: 316, cut 401).  Segments of fewer than 64 tokens do not pay for the two
-// launches more (5 rows of up to 333 tokens, 1048 channels: 33.4 us; of 128: 53).
+// price of passing over all but a row's last one twice.
+//
+// Which: uncut, 256 workgroups take as long as 128 (221 us for 2048 tokens of 8192 channels; cut 207 and
+// 130), 384 are as fast as cut (312 us for 308), and from there on cutting loses (512: 316, cut 401).
+//
+// How long: eight workgroups for each of 256 compute units (one prompt of 16384 x 4096: 420 us in segments of
+// 512 tokens, 456 of 1024, 526 of 2048).  Not under 64 tokens (5 rows of up to 333 tokens, 1048 channels: 29.6
+// us in segments of 64, 45 of 128, 28.5 of 32; 4096 tokens of 64 channels: 26.8, 32.5, 31.6), and not so many
+// that joining them, which each does with all before it, takes longer than passing over one: the root of the
+// chain's stages, and of the state's size (64 channels of 16384 tokens: 46.8 us in segments of 128, 55.6 of 64,
+// 57.8 of 256; of 65536: 85.8 of 256, 107 of 128 or 512).
 struct Cut {
     sqimpl::PromptPlan plan;
     int64_t tiles, segments, places, ws_bytes;
@@ -142,7 +147,9 @@ Cut cut_prompts(const sq_scan_shape_t *s, int xb, int sb) {
     int64_t tokens = sat_mul(s->n_seq, s->T);
     if (s->tokens > 0 && s->tokens < tokens) tokens = s->tokens;
     const int64_t chain = (std::min<int64_t>(s->T, tokens) + stage - 1) / stage;
-    const int64_t work = sat_mul(tokens / stage + 1, c.tiles), share = std::max(kLeast, work / kSlots);
+    const int64_t work = sat_mul(tokens / stage + 1, c.tiles);
+    const int64_t joins = (int64_t)std::sqrt((double)chain * ((s->d_state + 15) / 16)) / 4;
+    const int64_t share = std::max(std::max(kLeast, joins), work / kSlots);
     const int64_t segments = tokens / (share * stage) + s->n_seq;
     if (chain > 2 * kLeast && chain > 2 * share && work / chain < kBusy && sat_mul(segments, c.tiles) <= INT32_MAX) {
         c.seg_len = (int32_t)(share * stage);
@@ -281,7 +288,6 @@ int selscan_prefill(const sq_scan_shape_t *s, const sq_scan_data_t *p, void *sta
         a.ws = static_cast<float *>(workspace);
         a.ws_total = a.ws + c.places * c.tiles * c.plan.ws_floats;
         if ((rc = launch(c.plan.first, blocks, c.plan.threads, 0, &a, hip_stream)) != CV_OK) return rc;
-        if ((rc = launch(c.plan.combine, sat_mul(s->n_seq, c.tiles), c.plan.threads, 0, &a, hip_stream)) != CV_OK) return rc;
     }
     return launch(c.plan.run, blocks, c.plan.threads, 0, &a, hip_stream);
 }
@@ -319,7 +325,7 @@ int selscan_describe(int call, const sq_scan_shape_t *s, sq_scan_info_t *info) {
         info->threads = c.plan.threads;
         info->channels = c.plan.channels;
         info->workspace_bytes = c.ws_bytes;
-        if (c.ws_bytes) info->launches = 3, info->segment_tokens = c.seg_len;
+        if (c.ws_bytes) info->launches = 2, info->segment_tokens = c.seg_len;
         return CV_OK;
     }
     const sqimpl::ScanPlan p = plan_few(s, need, xb, sb);

@@ -25,7 +25,7 @@ struct ScanArgs {
     int32_t seg_len, segments;    // segments that the grid holds
     int32_t places;               // segments of cut rows that the workspace holds
     float *ws;                    // what each segment adds to a state (a row's last: the row's
-                                  // first state), then the state behind it
+                                  // first state)
     float *ws_total;              // each channel's sum of delta over each
 };
 
@@ -38,10 +38,9 @@ ScanPlan pick_scan(int x_bytes, int state_bytes, int d_state, bool one, bool out
 ScanPlan pick_groups(int x_bytes, int state_bytes, int d_state, int T);
 
 // Packed prompts.  run makes the outputs and the last state; where rows are cut, first leaves what
-// each segment adds to a state of zeros, and the row's first state, in the workspace, and combine
-// makes the state behind each segment of them.
+// each segment adds to a state of zeros, and the row's first state, in the workspace.
 struct PromptPlan {
-    const void *run, *first, *combine;
+    const void *run, *first;
     int channels, threads, stage;       // of a workgroup; tokens of a stage
     int64_t ws_floats, total_floats;    // of one workgroup's state, and of its sums of delta
 };

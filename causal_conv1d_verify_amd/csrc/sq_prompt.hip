@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
             return;
         }
     } else if (cut) {
-        from_workspace(seg.index > 0 ? seg.index - 1 : segments_of(a, seg.row) - 1);
+        from_workspace(segments_of(a, seg.row) - 1);
     } else if (init) {
         from_pool();
     }
@@ -135,6 +135,27 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
 #pragma unroll
             for (int r = 0; r < 4; ++r) decay[q][r] *= kLog2e;
         }
+    if (MAKES == PROMPT && cut) {                  // and what the segments before this one add to them
+        constexpr int AHEAD = NT == 1 ? 8 : NT == 2 ? 4 : 2;   // segments that are in flight at once
+        for (int s0 = 0; s0 < seg.index; s0 += AHEAD) {
+            float add[AHEAD][NT][4], total[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int64_t from = place(s0 + u < seg.index ? s0 + u : seg.index - 1);
+                total[u] = a.ws_total[from];
+#pragma unroll
+                for (int q = 0; q < NT; ++q) load_vec<4>(a.ws + from * NL + 4 * q, add[u][q]);
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (s0 + u < seg.index)
+#pragma unroll
+                    for (int q = 0; q < NT; ++q)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            h[q][r] = fmaf(h[q][r], __builtin_amdgcn_exp2f(total[u] * decay[q][r]), add[u][q][r]);
+        }
+    }
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = OUT && a.D ? a.D[c] : 0.0f;
 
     // ---- the tokens
@@ -258,49 +279,9 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
             if (16 * q + 4 * g < a.d_state) store_vec<4>(state + 16 * q, h[q]);
 }
 
-// Between the two: each segment's place in the workspace, which holds what its own tokens leave in a
-// state of zeros, is left with the state behind it, from the row's first state in the last one's place.
-template <int NT>
-__global__ __launch_bounds__(256) void combine(const ScanArgs a) {
-    const int tid = threadIdx.x;
-    const int tile = blockIdx.x % a.tiles, i = blockIdx.x / a.tiles;
-    const int count = uniform(segments_of(a, i));
-    if (count < 2) return;                         // same for the workgroup
-    const int64_t first = first_place<4>(a, i);
-    if (first + count > a.places) return;
-    const int c = tile * kChannels + 16 * (tid >> 6) + (tid & 15), n0 = 4 * (tid >> 4 & 3);
-    if (c >= a.d) return;
-    const int64_t step = (int64_t)a.tiles * 256, at = first * step + tile * 256 + tid;
-    constexpr int AHEAD = 8;                       // segments that are in flight at once
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-        float rate[4] = {}, h[4];
-        if (16 * q + n0 < a.d_state) load_vec<4>(a.A + (int64_t)c * a.d_state + 16 * q + n0, rate);
-        float *ws = a.ws + at * 4 * NT + 4 * q;
-        load_vec<4>(ws + (count - 1) * step * 4 * NT, h);
-        for (int s0 = 0; s0 < count - 1; s0 += AHEAD) {
-            float add[AHEAD][4], total[AHEAD];
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                const int64_t s = s0 + u < count - 1 ? s0 + u : count - 2;
-                load_vec<4>(ws + s * step * 4 * NT, add[u]);
-                total[u] = a.ws_total[at + s * step];
-            }
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u)
-                if (s0 + u < count - 1) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        h[r] = fmaf(h[r], __builtin_amdgcn_exp2f(total[u] * (rate[r] * kLog2e)), add[u][r]);
-                    store_vec<4>(ws + (s0 + u) * step * 4 * NT, h);
-                }
-        }
-    }
-}
-
 template <typename XT, typename ST, int NT>
 PromptPlan plan() {
-    return {(const void *)prompt<XT, ST, NT, 4, PROMPT>, (const void *)prompt<XT, ST, NT, 4, FIRST>, (const void *)combine<NT>,
+    return {(const void *)prompt<XT, ST, NT, 4, PROMPT>, (const void *)prompt<XT, ST, NT, 4, FIRST>,
             kChannels, 256, 16, 256 * 4 * NT, 256};
 }
 template <typename XT, typename ST, int NT>

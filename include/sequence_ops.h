@@ -127,7 +127,7 @@ typedef struct sq_scan_info {
     int32_t threads;        /* of a workgroup                                               */
     int32_t channels;       /* of a workgroup                                               */
     int32_t segment_tokens; /* prompts: tokens of a segment of a cut row; 0: none is cut    */
-    int32_t launches;       /* 3 where rows are cut, 0 where there is nothing to do         */
+    int32_t launches;       /* 2 where rows are cut, 0 where there is nothing to do         */
 } sq_scan_info_t;
 CV_API int selscan_describe(int call, const sq_scan_shape_t *shape, sq_scan_info_t *info);
 

@@ -36,7 +36,7 @@ static int sixteens(int d_state) { return (d_state + 15) / 16; }
 ScanPlan pick_scan(int, int, int d_state, bool, bool) { return {mark(0), d_state <= 16 ? 256 : d_state <= 32 ? 128 : 64, 256}; }
 ScanPlan pick_groups(int, int, int, int) { return {mark(1), 64, 256}; }
 PromptPlan pick_prompt(int, int, int d_state) {
-    return {mark(2), mark(3), mark(4), 64, 256, 16, 1024 * sixteens(d_state), 256};
+    return {mark(2), mark(3), 64, 256, 16, 1024 * sixteens(d_state), 256};
 }
 RotaryPlan pick_rotary(int, int dim) {
     const int units = dim / 16;
@@ -121,7 +121,7 @@ void scan_accepted(int call, const sq_scan_shape_t &s) {
     check((int64_t)g_launches.back().grid == info.workgroups, "workgroups described");
     for (const Launch &l : g_launches) {
         check((wide)l.scan.tiles * info.channels >= s.d && (wide)(l.scan.tiles - 1) * info.channels < s.d, "tiles");
-        check((wide)l.grid == (wide)(l.code == 4 ? s.n_seq : a.segments) * a.tiles, "workgroups");
+        check((wide)l.grid == (wide)a.segments * a.tiles, "workgroups");
     }
     check(g_launches.back().code == (call == SQ_SCAN_PREFILL ? 2 : g_launches.back().code == 1 ? 1 : 0), "kernel");
     if (g_launches.back().code >= 1) {             // four tokens lie within 2 GiB, and 16 of C
@@ -130,11 +130,11 @@ void scan_accepted(int call, const sq_scan_shape_t &s) {
             check(((wide)3 * t + s.d) * xb <= INT32_MAX, "far tokens");
     }
     if (call != SQ_SCAN_PREFILL) return;
-    if (info.launches != 3) {
+    if (info.launches != 2) {
         check(a.seg_len == s.T && a.segments == s.n_seq && info.workspace_bytes == 0, "whole rows");
         return;
     }
-    check(g_launches[0].code == 3 && g_launches[1].code == 4, "order of the launches");
+    check(g_launches[0].code == 3, "order of the launches");
     check(a.seg_len == info.segment_tokens && a.seg_len < s.T && a.seg_len % 16 == 0, "segments");
     const wide each = (wide)a.places * a.tiles, ws = (const char *)a.ws_total - (const char *)a.ws;
     check(a.places > 0 && ws == each * 4096 * sixteens(s.d_state) && ws + each * 1024 <= info.workspace_bytes, "workspace");
@@ -185,7 +185,7 @@ void scans(long n) {
             continue;
         }
         ++taken[call];
-        cut += g_launches.size() == 3;
+        cut += g_launches.size() == 2;
         scan_accepted(call, s);
     }
     std::printf("fuzz: %ld shapes, taken %ld %ld %ld %ld, cut %ld\n", n, taken[0], taken[1], taken[2], taken[3], cut);
