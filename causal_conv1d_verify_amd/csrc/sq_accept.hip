@@ -8,6 +8,10 @@
 // `sums` has a wavefront add up kPart weights each, over the whole card also for a single row; `pick`,
 // one workgroup a row, finds the part and then the weight at which the running sum passes the given
 // share of the total.  Sums are fp64, in an order that the sizes alone set.
+//
+// 128 rows of 128000 probabilities with drafts, 122 MB: 23 us, the copy's rate.  A few rows are latency: 7.8 us, 4.0
+// and 3.0 of the two kernels, three dependent loads each.  All of a row in one workgroup of 16 wavefronts and
+// one launch was no faster for 4000 probabilities (8.1 us for 8.2) and slower for more (32000: 10.0 for 8.8).
 #include "la_device.h"
 #include "sq_internal.h"
 

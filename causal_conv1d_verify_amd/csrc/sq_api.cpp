@@ -121,8 +121,9 @@ sqimpl::ScanArgs scan_args(const sq_scan_shape_t *s, const sq_scan_data_t *p, co
 // 64 channels unless few chains leave most of the chip idle; then rows are cut into segments, at the
 // price of passing over all but a row's last one twice.
 //
-// Which: uncut, 256 workgroups take as long as 128 (221 us for 2048 tokens of 8192 channels; cut 207 and
-// 130), 384 are as fast as cut (312 us for 308), and from there on cutting loses (512: 316, cut 401).
+// Which: where fewer than 256 workgroups, one for each compute unit, would be busy.  128 take 202 us for
+// 2048 tokens of 8192 channels and 125 cut, 256 203 either way; from there on cutting loses (384: 284 us
+// and 317 cut, 512: 285 and 401).
 //
 // How long: eight workgroups for each of 256 compute units (one prompt of 16384 x 4096: 420 us in segments of
 // 512 tokens, 456 of 1024, 526 of 2048).  Not under 64 tokens (5 rows of up to 333 tokens, 1048 channels: 29.6
@@ -136,7 +137,7 @@ struct Cut {
     int32_t seg_len;
 };
 Cut cut_prompts(const sq_scan_shape_t *s, int xb, int sb) {
-    constexpr int64_t kSlots = 2048, kBusy = 320;  // workgroups: of cut rows, and of uncut ones that are left so
+    constexpr int64_t kSlots = 2048, kBusy = 256;  // workgroups: of cut rows, and of uncut ones that are left so
     constexpr int64_t kLeast = 4;                  // stages
     Cut c{};
     c.plan = sqimpl::pick_prompt(xb, sb, s->d_state);

@@ -1,19 +1,33 @@
-// The selective scan of packed prompts: for each channel c and state n
+// The selective scan of packed prompts, and of 8 and more tokens of each row: for each channel c and
+// state n
 //
 //   h <- exp(delta A[c,n]) h + (delta x) B[n],   y = sum_n C[n] h + D x,   out = y silu(z)
 //
 // The decay is another one for every channel and state, so no product of matrices makes it: each
-// state update is a multiply, an exponential and two multiply-adds on the vector units (24 cycles of
-// a wavefront in all: 4 + 8 + 4 + 4, and 1.5 of the sum across lanes), which bound this kernel.  What can be taken off them is:
-// the products (delta x) B are a rank-one product for each token, four tokens of 16 states x 16
-// channels in one matrix instruction beside them.
+// state update is a multiply, an exponential and two multiply-adds on the vector units (4 + 8 + 4 + 4
+// cycles of a wavefront).  They bound this kernel: 8 x 2048 tokens of 8192 channels with 16 states take 494
+// us, of which the updates alone are 273 at 2.4 GHz; the stream of x, dt, z and out would take 204.  A
+// wavefront has 400 vector instructions for 64 updates of a lane, 256 of them theirs, 36 for each token of
+// a channel (conversions, softplus, gate, the sum across lanes); the vector units are 84-90% busy, at 2.1 to
+// 2.2 GHz.  What could be taken off them: the products (delta x) B are a rank-one product for each
+// token, four tokens of 16 states x 16 channels in one matrix instruction beside them (656 -> 591 us,
+// together with the layout below).
 //
 // A wavefront has 16 channels from a segment's first token to its last, lane l channel l % 16 and, of
 // every 16 states, the four from 4 (l / 16) on; tokens go in groups of four, of which lane l loads x, dt
 // and z of token l / 16 and makes its delta and gate.  The deltas of a group come back through LDS in
 // one vector, as C does (a stage of 16 tokens, converted once).  The four lanes' sums of four tokens
 // are added and dealt out in three lane swaps, to the lane that has the token.  Loads are a stage
-// ahead.  No barrier: wavefronts are alone.
+// ahead, without branches among them and waited for alone (591 -> 494 us with the instructions that
+// this saves).  No barrier: wavefronts are alone, four on a SIMD (of NT 1).
+//
+// Where rows are cut, `first` passes over all segments but a row's last one for what each adds to a state
+// of zeros, and each segment joins those before it: 1 x 16384 tokens of 4096 channels 418 us, 170 and 244
+// of the two kernels; uncut a token takes 99 ns.
+//
+// Tried and slower: the sums with C as 4 x 4 x 1 matrix instructions (678 us for 540: each keeps the SIMD for
+// some 13 cycles); the few tokens' states brought to their lanes through LDS from whole runs (128 rows of 8
+// tokens: 64.7 us for 59.4).
 #include "sq_scan_device.h"
 
 namespace sqimpl {

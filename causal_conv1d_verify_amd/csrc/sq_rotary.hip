@@ -1,5 +1,6 @@
 // The norm of each head of q and k and its rotation by the token's position, in one pass: a head is
-// read once and written once, and that traffic bounds it.
+// read once and written once, and that traffic bounds it (16384 tokens of 32 heads of 128 channels, half of
+// them rotated, bf16: 54.4 us, 4.9 TB/s, where a large copy has 5.3).
 //
 // A wavefront has one token (or some of its heads) and makes its angles once, one or two a lane, for
 // all heads: the product position * inv_freq and its remainder modulo a turn in fp64, then sine and
