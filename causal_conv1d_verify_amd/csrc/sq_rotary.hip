@@ -67,7 +67,7 @@ __device__ __forceinline__ float inverse_norm(float (&v)[16], float per_dim, flo
     float sum = total(), e = eps;
     const bool high = !(sum < INFINITY), low = sum < 0x1p-100f && eps < 0x1p-100f;
     if (__builtin_expect(high || low, 0)) {
-        const float scale = high ? 0x1p-80f : 0x1p80f;
+        const float scale = high ? 0x1p-80f : 0x1p100f;   // a square of 2^-149 2^100 is no subnormal, which rsq takes for 0
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] *= scale;
         sum = total();

@@ -175,3 +175,14 @@ def test_no_tokens():
     p = Problem(0, 2, 2, 64, 64, BF16)
     p.call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-40, 1e-44])
+def test_subnormal_heads(scale):
+    """Values that fp32 holds as subnormals (exactly, as the inputs' own), whose norm is an ordinary one."""
+    _say(scale)
+    p = Problem(9, 3, 2, 64, 32, F32)
+    p.rows.mul_(scale)
+    want = p.expect(eps=0.0)
+    p.call(eps=0.0)
+    p.check(want)
