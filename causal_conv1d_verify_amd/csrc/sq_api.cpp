@@ -107,7 +107,7 @@ sqimpl::ScanArgs scan_args(const sq_scan_shape_t *s, const sq_scan_data_t *p, co
     a.z_seq = s->z_seq_stride; a.z_tok = s->z_tok_stride;
     a.b_seq = s->b_seq_stride; a.b_tok = s->b_tok_stride;
     a.c_seq = s->c_seq_stride; a.c_tok = s->c_tok_stride;
-    a.o_seq = s->out_seq_stride; a.o_tok = s->out_tok_stride;
+    a.o_seq = s->out_seq_stride; a.o_tok = std::max<int64_t>(s->out_tok_stride, s->d);   // less: there is one token
     a.s_slot = s->state_slot_stride;
     a.n_seq = s->n_seq; a.T = s->T; a.d = s->d; a.d_state = s->d_state; a.n_slots = s->n_slots;
     a.softplus = s->softplus;

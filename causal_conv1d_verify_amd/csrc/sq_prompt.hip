@@ -47,8 +47,9 @@ __device__ __forceinline__ float deal_sums(const float (&p)[4]) {
 }
 
 // The elements of a segment's tokens that a wavefront loads or stores in groups of four tokens, each
-// through a buffer resource that ends with the segment's last token: loads past it are 0, and stores
-// are dropped, as at the offset kNowhere.
+// through a buffer resource that ends with the segment's last token: loads past it are 0 (or, where a
+// token's stride is below its width, of what overlaps with it), and stores are dropped, as at the
+// offset kNowhere.
 constexpr uint32_t kNowhere = 0x80000000u;
 template <typename XT>
 struct Tokens {
@@ -166,8 +167,13 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
 #pragma unroll
                     for (int q = 0; q < NT; ++q)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            h[q][r] = fmaf(h[q][r], __builtin_amdgcn_exp2f(total[u] * decay[q][r]), add[u][q][r]);
+                        for (int r = 0; r < 4; ++r) {
+                            // 2^e in two factors: a whole segment's may leave fp32's range where the state
+                            // does not, and 0 stays 0 (a total that is not finite is in `add` as well)
+                            const float e = __builtin_amdgcn_fmed3f(total[u] * decay[q][r], -1024.0f, 1024.0f);
+                            const float whole = rintf(e), grown = h[q][r] * __builtin_amdgcn_exp2f(e - whole);
+                            h[q][r] = __builtin_ldexpf(grown, (int)whole) + add[u][q][r];
+                        }
         }
     }
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = OUT && a.D ? a.D[c] : 0.0f;
@@ -191,7 +197,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
     XT next_x[K], next_dt[K], next_z[K], next_b[K][NT];
     Run<XT, NL> next_c;
     // The stage from token s on.  There is no branch among its loads, which would wait for them:
-    // past the row's end x, dt, z and B are 0, and C the last token's, for outputs that nobody has.
+    // past the row's end C is the last token's, for outputs that nobody has.
     auto fetch = [&](int s) {
         if constexpr (OUT) {
             const XT *p = C + s * a.c_tok + off_c;
@@ -211,7 +217,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
         }
     };
     float total = 0.0f;
-    fetch(0);
+    if (n > 0) fetch(0);                           // (a row of no tokens has no last one to load)
     // The first stage's loads are waited for here: with none under way into the loop, its own wait is for
     // a stage's loads alone and not for the stores behind them.
     if (CUTS) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
@@ -243,9 +249,15 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
                 const float open = gate(gates[k]);   // (without z that of x, which nobody has)
                 gates[k] = a.z ? open : 1.0f;
             }
-        if (s + STAGE > n)                        // past the last token nothing changes
+        if (s + STAGE > n)                        // past the last token nothing changes, whatever lies there
 #pragma unroll
-            for (int k = 0; k < K; ++k) delta[k] = s + 4 * k + g < n ? delta[k] : 0.0f;
+            for (int k = 0; k < K; ++k) {
+                const bool is = s + 4 * k + g < n;
+                delta[k] = is ? delta[k] : 0.0f;
+                xv[k] = is ? xv[k] : 0.0f;
+#pragma unroll
+                for (int q = 0; q < NT; ++q) b[k][q] = is ? b[k][q] : 0.0f;
+            }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             deltas[wave][k][j][g] = delta[k];
@@ -277,7 +289,8 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
                 }
             }
             if constexpr (OUT) {
-                store_to<XT>(out.from(s + 4 * k, n), off_out, fmaf(skip, xv[k], deal_sums(sum)) * gates[k]);
+                const float y = deal_sums(sum), with = fmaf(skip, xv[k], y);
+                store_to<XT>(out.from(s + 4 * k, n), off_out, (a.D ? with : y) * gates[k]);
             }
         }
     }

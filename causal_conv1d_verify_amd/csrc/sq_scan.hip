@@ -127,8 +127,8 @@ __global__ __launch_bounds__(256) void scan(const ScanArgs a) {
 #pragma unroll
             for (int k = 0; k < G; ++k) {
                 if (s + k >= n) break;
-                const float y = fmaf(skip, xv[k], sums[wave][k][lane & (CH - 1)]) * gates[k];
-                if (mine) store_one(out + k * a.o_tok + c, y);
+                const float y = sums[wave][k][lane & (CH - 1)], with = fmaf(skip, xv[k], y);
+                if (mine) store_one(out + k * a.o_tok + c, (a.D ? with : y) * gates[k]);
             }
         }
     }

@@ -57,7 +57,8 @@ extern "C" {
  *    tokens of x, dt, z, B and out, and any 16 of C, within 2 GiB.
  *  - Numerics: delta, decays, states and sums are held in fp32.  A state stored as bf16 is rounded
  *    once, after the last token of the call.  A token's values that are not finite change the
- *    outputs of their own and of later tokens only (x, dt, z: of their own channel).
+ *    outputs of their own and of later tokens only (x, dt, z: of their own channel), which
+ *    are not finite then and may be NaN where the formula has an infinity.
  */
 typedef struct sq_scan_shape {
     int32_t n_seq;        /* rows, >= 0 (0: nothing to do)                                  */

@@ -400,3 +400,64 @@ def test_two_calls_at_once():
             prefill(p)
     for p, want in zip(ps, wants):
         p.check(want)
+
+
+@pytest.mark.parametrize("d,n", [(64, 16), (72, 24), (24, 64)])
+def test_rows_of_no_tokens_at_either_end(d, n):
+    _say("no tokens at either end", d, n)
+    p = Problem([0, 0, 21, 0], d, n, "bf16_f32", packed=True, started=[0, 1, 0, 0])
+    want = p.expect()
+    prefill(p)
+    p.check(want)
+
+
+@pytest.mark.parametrize("kind,tokens", [("prefill", 1), ("prefill", 5), ("prefill", 18), ("update", 9), ("update", 18)])
+@pytest.mark.parametrize("where", ["x", "B"])
+def test_an_infinity_in_every_token(kind, tokens, where):
+    """x or B is one row for all tokens, with an infinity: a state that it reaches is that infinity, not
+    what 0 times it would be for tokens past the row's end."""
+    _say("infinity", kind, tokens, where)
+    d, n = 64, 16
+    row = torch.ones(d if where == "x" else n, device="cuda")
+    row[3] = float("inf")
+    lead = (tokens,) if kind == "prefill" else (2, tokens)
+    x = row.expand(*lead, d) if where == "x" else torch.ones(*lead, d, device="cuda")
+    B = row.expand(*lead, n) if where == "B" else torch.ones(*lead, n, device="cuda")
+    dt, C = torch.zeros(*lead, d, device="cuda"), torch.ones(*lead, n, device="cuda")
+    A = -torch.ones(d, n, device="cuda")
+    state, out = torch.ones(2, d, n, device="cuda"), torch.zeros(*lead, d, device="cuda")
+    if kind == "prefill":
+        cu = torch.tensor([0, tokens], dtype=torch.int32).cuda()
+        _cv().selective_scan_prefill(x, dt, A, B, C, state, out, cu, max_len=tokens)
+        state, out = state[:1], out[None]
+    else:
+        _cv().selective_scan_update(x, dt, A, B, C, state, out)
+    hit = torch.zeros(d, n, dtype=torch.bool)
+    (hit[3] if where == "x" else hit[:, 3]).fill_(True)
+    assert torch.equal(torch.isposinf(state).cpu(), hit.expand(state.shape))
+    assert torch.isfinite(state.cpu()[~hit.expand(state.shape)]).all()
+    assert torch.equal(torch.isposinf(out).cpu(), hit.any(1).expand(out.shape))
+    assert torch.isfinite(out.cpu()[~hit.any(1).expand(out.shape)]).all()
+
+
+@pytest.mark.parametrize("n", [16, 24, 64])
+def test_growth_of_nothing(n):
+    """A state of zeros stays zeros however much it would have grown (e^4 a token, over segments of 64
+    and more), and the last token's values are whole numbers."""
+    _say("growth of nothing", n)
+    tokens, d = 1024, 64
+    x = torch.zeros(tokens, d, device="cuda")
+    x[-1] = -2.0
+    dt = torch.full((tokens, d), -1.0, device="cuda")
+    A = torch.full((d, n), -4.0, device="cuda")
+    B, C = torch.ones(tokens, n, device="cuda"), torch.ones(tokens, n, device="cuda")
+    state, out = torch.ones(1, d, n, device="cuda"), torch.full((tokens, d), POISON, device="cuda")
+    cu = torch.tensor([0, tokens], dtype=torch.int32).cuda()
+    kw = dict(max_len=tokens, dt_softplus=False, has_initial_state=torch.zeros(1, dtype=torch.int32).cuda())
+    import causal_conv1d_verify_amd.sequence_ops as sq
+
+    assert sq.selective_scan_describe("prefill", x, dt, A, B, C, state, out, cu, **kw).segment_tokens > 0
+    _cv().selective_scan_prefill(x, dt, A, B, C, state, out, cu, **kw)
+    assert torch.equal(state.cpu(), torch.full((1, d, n), 2.0))
+    assert torch.equal(out[:-1].cpu(), torch.zeros(tokens - 1, d))
+    assert torch.equal(out[-1].cpu(), torch.full((d,), 2.0 * n))
