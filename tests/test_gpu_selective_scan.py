@@ -461,3 +461,16 @@ def test_growth_of_nothing(n):
     assert torch.equal(state.cpu(), torch.full((1, d, n), 2.0))
     assert torch.equal(out[:-1].cpu(), torch.zeros(tokens - 1, d))
     assert torch.equal(out[-1].cpu(), torch.full((d,), 2.0 * n))
+
+
+@pytest.mark.parametrize("pair", PAIRS)
+@pytest.mark.parametrize("T", [8, 9, 12, 13, 20, 21, 24, 25])
+@pytest.mark.parametrize("d,n", [(64, 16), (40, 24), (24, 48), (16, 64)])
+def test_few_tokens_in_stages(pair, T, d, n):
+    """A group of four tokens more and less than the stages hold."""
+    _say("stages", pair, T, d, n)
+    for kind, write in (("selective_scan_verify", False), ("selective_scan_update", True)):
+        p = Problem([T] * 3, d, n, pair, packed=False, T=T, pads=(1,), seed=T + n)
+        want = p.expect(writes=write)
+        getattr(_cv(), kind)(p.x, p.dt, p.A, p.B, p.C, p.pool, p.out, **p.kw())
+        p.check(want)
