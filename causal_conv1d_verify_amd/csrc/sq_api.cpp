@@ -163,8 +163,8 @@ Cut cut_prompts(const sq_scan_shape_t *s, int xb, int sb) {
 }
 
 // Outputs of 8 and more tokens go in groups of four as prompts do, where a token takes fewer
-// instructions (16 states; 8 rows of 17: 10.2 us for 12.9, 128 rows of 8: 58.5 for 60.2, of 17: 121 for
-// 125, of 32: 164 for 206), with over 32 states of 4 and more (64 rows of 4, 64 states: 32.8 for 36.2, of
+// instructions (16 states; 8 rows of 17: 9.6 us for 12.9, 128 rows of 8: 58.5 for 60.2, of 17: 107 for
+// 125, of 32: 156 for 206), with over 32 states of 4 and more (64 rows of 4, 64 states: 32.8 for 36.2, of
 // 8: 38.9 for 65).  For fewer the state's way in counts, which that kernel has in pieces of 16
 // bytes (128 rows of 4: 45 us for 35; 256 rows of 1: 105 for 47 and more), and its 16 states at least (8
 // states, 64 rows of 8: 13 us for 10).  Tokens too far apart for its offsets go the other way too.

@@ -8,7 +8,7 @@
 // cycles of a wavefront).  They bound this kernel: 8 x 2048 tokens of 8192 channels with 16 states take 494
 // us, of which the updates alone are 273 at 2.4 GHz; the stream of x, dt, z and out would take 204.  A
 // wavefront has 400 vector instructions for 64 updates of a lane, 256 of them theirs, 36 for each token of
-// a channel (conversions, softplus, gate, the sum across lanes); the vector units are 84-90% busy, at 2.1 to
+// a channel (conversions, softplus, gate, the sum across lanes); the vector units are 82-90% busy, at 2.1 to
 // 2.2 GHz.  What could be taken off them: the products (delta x) B are a rank-one product for each
 // token, four tokens of 16 states x 16 channels in one matrix instruction beside them (656 -> 591 us,
 // together with the layout below).
