@@ -225,12 +225,14 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
         float xv[K], dx[K], gates[K], b[K][NT];
         // LDS of a wavefront is written and read in its own order
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if constexpr (OUT)
+        if constexpr (OUT) {
+            next_c.end(n0, a.d_state);
 #pragma unroll
             for (int i = 0; i < NL; i += 4) {
                 const float f[4] = {next_c[i], next_c[i + 1], next_c[i + 2], next_c[i + 3]};
                 store_vec<4>(&cs[wave][tc][n0 + i], f);
             }
+        }
         float delta[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {

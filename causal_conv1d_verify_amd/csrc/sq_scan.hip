@@ -27,6 +27,7 @@ __device__ __forceinline__ float quad_sum(float v) {
 template <typename XT, typename ST, int NL, int U, int G, bool OUT>
 __global__ __launch_bounds__(256) void scan(const ScanArgs a) {
     constexpr int CH = 16 * U;                     // channels of a wavefront
+    constexpr bool FITS = NL <= 8;                 // 4 NL is d_state; above, 40 and 56 go as 48 and 64
     __shared__ float2 steps[4][G][64];
     __shared__ float sums[4][G][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -50,7 +51,7 @@ __global__ __launch_bounds__(256) void scan(const ScanArgs a) {
     const int64_t z_tok = OUT && a.z ? a.z_tok : a.x_tok;
     struct Raw {
         XT x, dt, z;
-        Run<XT, NL> B, C;
+        Run<XT, NL, FITS> B, C;
     } next[G];
     auto fetch = [&](int s) {                      // past the last token it again: loads without branches
 #pragma unroll
@@ -73,10 +74,12 @@ __global__ __launch_bounds__(256) void scan(const ScanArgs a) {
     for (int u = 0; u < U; ++u) {
         const int cu = c0 + 16 * u + quad < a.d ? c0 + 16 * u + quad : a.d - 1;
         const int64_t at = (int64_t)cu * a.d_state;
-        Run<ST, NL> first;
-        Run<float, NL> rate;
+        Run<ST, NL, FITS> first;
+        Run<float, NL, FITS> rate;
         first.load(state + at, n0, a.d_state);
         rate.load(a.A + at, n0, a.d_state);
+        first.end(n0, a.d_state);
+        rate.end(n0, a.d_state);
 #pragma unroll
         for (int e = 0; e < NL; ++e) h[u][e] = first[e], decay[u][e] = rate[e] * kLog2e;
     }
@@ -85,7 +88,11 @@ __global__ __launch_bounds__(256) void scan(const ScanArgs a) {
         Raw now[G];
         float xv[G], gates[G];
 #pragma unroll
-        for (int k = 0; k < G; ++k) now[k] = next[k];
+        for (int k = 0; k < G; ++k) {
+            now[k] = next[k];
+            now[k].B.end(n0, a.d_state);
+            if constexpr (OUT) now[k].C.end(n0, a.d_state);
+        }
         // LDS of a wavefront is written and read in its own order
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll

@@ -21,27 +21,28 @@ typedef uint32_t u32x2_4 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // The NL consecutive elements from n0 on of a row of `count` (a multiple of 8), as they lie in memory.
-// Quads past the row (there are some only where NL is over 8) are 0, and what is loaded for them the
-// row's first: no branch among loads.
-template <typename XT, int NL>
+// Four lanes share a row, from 0, NL, 2 NL and 3 NL on.  FITS: that is the row exactly, as for sq_scan.hip's
+// rows of up to 32.  Otherwise runs may reach past it (its rows of 40 and 56, and sq_prompt.hip's, rounded up
+// to sixteens, of 8, 24, 40 and 56): for quads behind the row its first is loaded, without a branch among
+// loads, and `end` makes them 0, where the loads are waited for anyway.
+template <typename XT, int NL, bool FITS = false>
 struct Run {
     static constexpr int W = NL * (int)sizeof(XT) / 4;
-    static constexpr bool kWhole = NL <= 8;
+    static_assert(FITS || NL % 4 == 0, "only quads are held against the row's end");
     uint32_t w[W];
     __device__ __forceinline__ void load(const XT *row, int n0, int count) {
         if constexpr (NL % 4 == 0) {
 #pragma unroll
             for (int i = 0; i < NL; i += 4) {
-                const bool in = kWhole || n0 + i < count;
-                const XT *p = row + (in ? n0 + i : 0);
+                const XT *p = row + (FITS || n0 + i < count ? n0 + i : 0);
                 if constexpr (sizeof(XT) == 2) {
                     const u32x2_2 v = load_as<false, u32x2_2>(p);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) w[i / 2 + e] = in ? v[e] : 0;
+                    for (int e = 0; e < 2; ++e) w[i / 2 + e] = v[e];
                 } else {
                     const u32x4_4 v = load_as<false, u32x4_4>(p);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[i + e] = in ? v[e] : 0;
+                    for (int e = 0; e < 4; ++e) w[i + e] = v[e];
                 }
             }
         } else {
@@ -54,6 +55,11 @@ struct Run {
                     w[i] = v[0], w[i + 1] = v[1];
                 }
         }
+    }
+    __device__ __forceinline__ void end(int n0, int count) {
+        if constexpr (!FITS)
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = n0 + i * NL / W / 4 * 4 < count ? w[i] : 0;
     }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (sizeof(XT) == 2) return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
