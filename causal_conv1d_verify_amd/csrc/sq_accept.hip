@@ -289,7 +289,9 @@ __global__ __launch_bounds__(256) void pick(const AcceptArgs a) {
     for (int k = first; k < last && over < 0; ++k) {
         const double s = sums[k];
         if (s > 0.0) some = k;
-        if (at + s > passed) over = k;
+        // (`base` may be past `passed` where the sums before it, in their own order, are not: an empty
+        // part is not the one)
+        if ((s > 0.0) & (at + s > passed)) over = k;
         else at += s;
     }
     const Ends parts = ends_of(over >= 0, over, some >= 0, some, slots[0]);
