@@ -170,7 +170,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
                         for (int r = 0; r < 4; ++r) {
                             // 2^e in two factors: a whole segment's may leave fp32's range where the state
                             // does not, and 0 stays 0 (a total that is not finite is in `add` as well)
-                            const float e = __builtin_amdgcn_fmed3f(total[u] * decay[q][r], -1024.0f, 1024.0f);
+                            const float e = __builtin_amdgcn_fmed3f(exponent(total[u], decay[q][r]), -1024.0f, 1024.0f);
                             const float whole = rintf(e), grown = h[q][r] * __builtin_amdgcn_exp2f(e - whole);
                             h[q][r] = __builtin_ldexpf(grown, (int)whole) + add[u][q][r];
                         }
@@ -284,7 +284,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
                     if constexpr (OUT) w = *reinterpret_cast<const f32x4 *>(&cs[wave][4 * k + t][16 * q + 4 * g]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float keep = __builtin_amdgcn_exp2f(step[t] * decay[q][r]);
+                        const float keep = __builtin_amdgcn_exp2f(exponent(step[t], decay[q][r]));
                         h[q][r] = fmaf(h[q][r], keep, add[4 * t + r]);
                         if constexpr (OUT) sum[t] = fmaf(w[r], h[q][r], sum[t]);
                     }

@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256) void scan(const ScanArgs a) {
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < NL; ++e) {
-                    const float keep = __builtin_amdgcn_exp2f(step.x * decay[u][e]);
+                    const float keep = __builtin_amdgcn_exp2f(exponent(step.x, decay[u][e]));
                     h[u][e] = fmaf(h[u][e], keep, step.y * now[k].B[e]);
                     if constexpr (OUT) sum = fmaf(now[k].C[e], h[u][e], sum);
                 }

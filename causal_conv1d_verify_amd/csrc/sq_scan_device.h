@@ -84,6 +84,13 @@ __device__ __forceinline__ void store_run(ST *p, const float (&h)[NL], int left)
     }
 }
 
+// What a step, or a sum of steps, makes of a rate: the state keeps 2^ of it.  0 times anything is 0 here: a
+// step of nothing keeps a state also where its rate times log2 e is past fp32 (A of fp32's lowest value), and
+// a rate of 0 keeps it where a sum of steps is.  One instruction (for which the compiler has no builtin), no
+// slower than another product.
+extern "C" __device__ float scan_mul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float exponent(float step, float rate) { return scan_mul_legacy(step, rate); }
+
 // max(v, 0) + log(1 + e) with e = 2^(-|v| log2 e).  log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3: a
 // polynomial in s^2 keeps its relative accuracy where e is small, as 1 + e would not.
 __device__ __forceinline__ float softplus(float v) {
