@@ -371,9 +371,14 @@ def accept_drafts(tokens, target, uniform, num_tokens, next_token, *, draft=None
     the next token.  A draft outside [0, vocab) (a pad) is not tried, a row of a negative slot is not
     written.
 
-    Written, int32: num_tokens [n_seq], 1..T, as linear_attn_commit and selective_scan_commit take
-    it; next_token [n_seq]; window_index [n_seq] (if given), the last accepted token's place, as
-    conv_verify_restore takes it; path [n_seq, T] (if given), the accepted places, then -1."""
+    Written, int32: num_tokens [n_seq], 1..T; next_token [n_seq]; window_index [n_seq] (if given), the
+    last accepted token's place, as conv_verify_restore takes it; path [n_seq, T] (if given), the
+    accepted places, then -1.
+
+    linear_attn_commit and selective_scan_commit fold a row's first num_tokens tokens.  Of a chain those
+    are the accepted ones; of a tree they are not: gather the commit's inputs along path first (its -1
+    as any place), x.gather(1, path.clamp(min=0)...), and each row starts with its accepted tokens.
+    (Both layers' verifies follow a row's tokens in order; a tree goes through them branch by branch.)"""
     if stream is None and _done(_short().accept(tokens, target, uniform, num_tokens, next_token, draft,
                                                 parent, window_index, path, slot_idx, workspace)):
         return

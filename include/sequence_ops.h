@@ -196,7 +196,9 @@ CV_API int norm_rotary(const sq_rotary_shape_t *shape, const void *q, const void
  *   uniform      [n_seq, T] fp32 in [0, 1)
  *   slot_idx     [n_seq] int32 or NULL: a row of a negative slot is padded: nothing of it is written
  * Outputs, int32:
- *   num_tokens   [n_seq] the tokens to commit: token 0 and the accepted drafts, 1..T
+ *   num_tokens   [n_seq] how many tokens to commit: token 0 and the accepted drafts, 1..T.  Of a chain they
+ *                are the row's first ones, which selscan_commit and linattn_commit fold; of a tree path
+ *                names them, and a commit's inputs are to be gathered along it first
  *   next_token   [n_seq] the token drawn
  *   window_index [n_seq] or NULL: the last accepted token's place in the row (a chain: num_tokens - 1)
  *   path         [n_seq, T] or NULL: the places of the tokens to commit, then -1
