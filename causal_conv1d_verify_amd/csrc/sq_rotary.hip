@@ -5,8 +5,8 @@
 // A wavefront has one token (or some of its heads) and makes its angles once, one or two a lane, for
 // all heads: the product position * inv_freq and its remainder modulo a turn in fp64, then sine and
 // cosine by their series on an eighth of a turn.  They go through LDS.  A head lies across LG lanes, 16
-// channels each, in the two vectors of 8 that hold both halves of 8 rotated pairs: channels 8u and
-// rot/2 + 8u of unit u (interleaved: 16u and 16u + 8; behind the rotated ones likewise).
+// channels each, in two vectors of 8: from channels 8u and rot/2 + 8u on for unit u, which hold both halves
+// of 8 rotated pairs (interleaved: four whole pairs each); behind the rotated ones likewise.
 #include "la_device.h"
 #include "sq_internal.h"
 

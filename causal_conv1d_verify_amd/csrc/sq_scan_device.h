@@ -10,7 +10,6 @@ namespace {
 
 using namespace laimpl;
 
-constexpr int kStage = 16;        // tokens
 constexpr int kChannels = 64;     // of a workgroup, 16 of a wavefront
 constexpr float kLog2e = 1.4426950408889634f;
 

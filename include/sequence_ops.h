@@ -37,7 +37,8 @@ extern "C" {
  *   delta    = softplus(dt[t,c] + dt_bias[c])       (softplus = 0: dt[t,c] + dt_bias[c])
  *   h[c,n]   = exp(delta A[c,n]) h[c,n] + delta x[t,c] B[t,n]
  *   y        = sum_n C[t,n] h[c,n] + D[c] x[t,c]
- *   out[t,c] = y z[t,c] / (1 + exp(-z[t,c]))        rounded once to the x dtype; z NULL: y
+ *   out[t,c] = y z[t,c] / (1 + exp(-z[t,c]))        rounded once to the x dtype; z NULL: y (its
+ *                                                   strides are checked all the same: 0 will do)
  *
  *  - Layouts.  With packed rows (prefill) token t of row i is row cu_seqlens[i] + t and the seq
  *    strides are unused:
@@ -56,9 +57,10 @@ extern "C" {
  *    aligned, their strides multiples of 16 bytes; B and C aligned to their elements; prefill: any four
  *    tokens of x, dt, z, B and out, and any 16 of C, within 2 GiB.
  *  - Numerics: delta, decays, states and sums are held in fp32.  A state stored as bf16 is rounded
- *    once, after the last token of the call.  A token's values that are not finite change the
- *    outputs of their own and of later tokens only (x, dt, z: of their own channel), which
- *    are not finite then and may be NaN where the formula has an infinity.
+ *    once, after the last token of the call.  Decays, softplus and the gate's sigmoid count as 0
+ *    below 2^-126, fp32's normal range (z or dt + dt_bias under -87).  A token's values that are not
+ *    finite change the outputs of their own and of later tokens only (x, dt, z: of their own
+ *    channel), which are not finite then and may be NaN where the formula has an infinity.
  */
 typedef struct sq_scan_shape {
     int32_t n_seq;        /* rows, >= 0 (0: nothing to do)                                  */
