@@ -5,9 +5,9 @@
 //
 // The decay is another one for every channel and state, so no product of matrices makes it: each
 // state update is a multiply, an exponential and two multiply-adds on the vector units (4 + 8 + 4 + 4
-// cycles of a wavefront).  They bound this kernel: 8 x 2048 tokens of 8192 channels with 16 states take 494
+// cycles of a wavefront).  They bound this kernel: 8 x 2048 tokens of 8192 channels with 16 states take 498
 // us, of which the updates alone are 273 at 2.4 GHz; the stream of x, dt, z and out would take 204.  A
-// wavefront has 400 vector instructions for 64 updates of a lane, 256 of them theirs, 36 for each token of
+// wavefront has 402 vector instructions for 64 updates of a lane, 256 of them theirs, 36 for each token of
 // a channel (conversions, softplus, gate, the sum across lanes); the vector units are 82-90% busy, at 2.1 to
 // 2.2 GHz.  What could be taken off them: the products (delta x) B are a rank-one product for each
 // token, four tokens of 16 states x 16 channels in one matrix instruction beside them (656 -> 591 us,
@@ -16,13 +16,15 @@
 // A wavefront has 16 channels from a segment's first token to its last, lane l channel l % 16 and, of
 // every 16 states, the four from 4 (l / 16) on; tokens go in groups of four, of which lane l loads x, dt
 // and z of token l / 16 and makes its delta and gate.  The deltas of a group come back through LDS in
-// one vector, as C does (a stage of 16 tokens, converted once).  The four lanes' sums of four tokens
+// one vector, as C does (a stage of 16 tokens, converted once).  States come in sixteens: 8, 24, 40 and 56 of
+// them take the time of 16, 32, 48 and 64, with zeros in the last places (8 x 1024 tokens of 8192 channels: 249
+// and 253 us with 8 and 16 states, 408 and 409 with 24 and 32, 596 with 40 and 48, 831 with 56 and 64).  The four lanes' sums of four tokens
 // are added and dealt out in three lane swaps, to the lane that has the token.  Loads are a stage
 // ahead, without branches among them and waited for alone (591 -> 494 us with the instructions that
 // this saves).  No barrier: wavefronts are alone, four on a SIMD (of NT 1).
 //
 // Where rows are cut, `first` passes over all segments but a row's last one for what each adds to a state
-// of zeros, and each segment joins those before it: 1 x 16384 tokens of 4096 channels 418 us, 170 and 244
+// of zeros, and each segment joins those before it: 1 x 16384 tokens of 4096 channels 418 us, 166 and 252
 // of the two kernels; uncut a token takes 99 ns.
 //
 // Tried and slower: the sums with C as 4 x 4 x 1 matrix instructions (678 us for 540: each keeps the SIMD for
