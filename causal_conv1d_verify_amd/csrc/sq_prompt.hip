@@ -16,12 +16,14 @@
 // A wavefront has 16 channels from a segment's first token to its last, lane l channel l % 16 and, of
 // every 16 states, the four from 4 (l / 16) on; tokens go in groups of four, of which lane l loads x, dt
 // and z of token l / 16 and makes its delta and gate.  The deltas of a group come back through LDS in
-// one vector, as C does (a stage of 16 tokens, converted once).  States come in sixteens: 8, 24, 40 and 56 of
-// them take the time of 16, 32, 48 and 64, with zeros in the last places (8 x 1024 tokens of 8192 channels: 249
-// and 253 us with 8 and 16 states, 408 and 409 with 24 and 32, 596 with 40 and 48, 831 with 56 and 64).  The four lanes' sums of four tokens
+// one vector, as C does (a stage of 16 tokens, converted once).  The four lanes' sums of four tokens
 // are added and dealt out in three lane swaps, to the lane that has the token.  Loads are a stage
 // ahead, without branches among them and waited for alone (591 -> 494 us with the instructions that
 // this saves).  No barrier: wavefronts are alone, four on a SIMD (of NT 1).
+//
+// States come in sixteens: 8, 24, 40 and 56 of them take the time of 16, 32, 48 and 64, with zeros in the last
+// places (8 x 1024 tokens of 8192 channels: 249 and 253 us with 8 and 16 states, 408 and 409 with 24 and
+// 32, 596 with 40 and 48, 831 with 56 and 64).
 //
 // Where rows are cut, `first` passes over all segments but a row's last one for what each adds to a state
 // of zeros, and each segment joins those before it: 1 x 16384 tokens of 4096 channels 418 us, 166 and 252
@@ -171,7 +173,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : NT == 2 ? 3 : 2) void prompt(con
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             // 2^e in two factors: a whole segment's may leave fp32's range where the state
-                            // does not, and 0 stays 0 (a total that is not finite is in `add` as well)
+                            // does not, and 0 stays 0 (a token's delta that is not finite is in `add` as well)
                             const float e = __builtin_amdgcn_fmed3f(exponent(total[u], decay[q][r]), -1024.0f, 1024.0f);
                             const float whole = rintf(e), grown = h[q][r] * __builtin_amdgcn_exp2f(e - whole);
                             h[q][r] = __builtin_ldexpf(grown, (int)whole) + add[u][q][r];

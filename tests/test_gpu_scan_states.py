@@ -99,3 +99,28 @@ def test_a_later_token_stays_out_of_earlier_ones(where, value, call, n):
     same[first:end if where == "B" else token + 1] = False
     assert torch.equal(outs[0][same], outs[1][same])
     assert not torch.isfinite(outs[1][token].float()).any()
+
+
+@pytest.mark.parametrize("where", ["x", "dt", "z"])
+@pytest.mark.parametrize("value", [NAN, float("inf")])
+@pytest.mark.parametrize("call", ["prompts", "cut", "verify9", "update3"])
+@pytest.mark.parametrize("n", STATES)
+def test_a_channel_stays_out_of_the_others(where, value, call, n):
+    """x, dt or z of one channel of a later token: its own channel from there on (z: there) alone."""
+    print("[case]", where, value, call, n, flush=True)
+    token = {"prompts": 30, "cut": 350, "verify9": 13, "update3": 4}[call]
+    end = {"prompts": 52, "cut": 700, "verify9": 18, "update3": 6}[call]
+    outs = []
+    for bad in (False, True):
+        kind, p = _problem(call, n, "bf16_f32")
+        _place(p, None)
+        if bad:
+            t = getattr(p, where)
+            t[(token,) if t.dim() == 2 else (token // p.T, token % p.T)][21] = value
+        _call(kind, p)
+        torch.cuda.synchronize()
+        outs.append(p.out.reshape(p.tokens, p.d))
+    same = torch.ones(p.tokens, p.d, dtype=torch.bool)
+    same[token:token + 1 if where == "z" else end, 21] = False
+    assert torch.equal(outs[0][same], outs[1][same])
+    assert not torch.isfinite(outs[1][token, 21].float())
